@@ -112,11 +112,14 @@ typedef struct {
 typedef enum {
   GPTQ_OP_HESSIAN = 0,
   GPTQ_OP_PREPARE_HINV = 1,
-  GPTQ_OP_QUANTIZE = 2
+  GPTQ_OP_QUANTIZE = 2,
+  GPTQ_OP_LORA_BACKWARD = 3
 } gptq_op;
 
 /* Bytes of workspace `op` needs for the given sizes (n is ignored except by
- * GPTQ_OP_HESSIAN; cfg may be NULL for GPTQ_OP_HESSIAN).  0 means none. */
+ * GPTQ_OP_HESSIAN and GPTQ_OP_LORA_BACKWARD; cfg may be NULL except for
+ * GPTQ_OP_QUANTIZE).  0 means none.  GPTQ_OP_LORA_BACKWARD: r = the adapters'
+ * rank, n = tokens (rows of dY), k is ignored. */
 GPTQ_API size_t gptq_workspace_size(int op, int64_t r, int64_t k, int64_t n, const gptq_config* cfg);
 
 /* Human-readable name of a status code (static storage). */
@@ -340,6 +343,110 @@ GPTQ_API gptq_status gptq_gemm(const void* X, gptq_dtype dt, int64_t m, int64_t 
 GPTQ_API gptq_status gptq_rotate(const void* in, gptq_dtype dt, int64_t rows, int64_t k,
                         int64_t ld_in, const int8_t* signs, int block, int inverse, void* out,
                         int64_t ld_out, gptq_stream_t stream);
+
+/* The gradient of gptq_gemm with respect to its input, read straight from the
+ * packed codes (what a step that trains through a frozen quantized layer hands
+ * to the layer below):
+ *   dX[t, c] = sum_j dY[t, j] * scales[j, g] * (code[j, c] - zeros[j, g]),
+ *   g = g_idx[c], or c / group_size when g_idx is NULL,
+ * summed in fp32 and rounded once to dt.
+ *   dY      (m, n) f16 or bf16 (dt), row-major, leading dimension lddy >= n.
+ *   qweight, scales, zeros, g_idx, bits, group_size, ngroups  as for gptq_gemm.
+ *   dX      (m, k) out, dt, row-major, leading dimension lddx >= k.  Must not
+ *           overlap dY.
+ *   m <= 131070 tokens.  The library allocates nothing.
+ * Kernel choice:
+ *   4-bit, g_idx NULL, group_size a multiple of 8 (or one group per row), dY
+ *     16-byte aligned with lddy % 8 == 0 and qweight 16-byte aligned: the
+ *     tensor-core kernel (each weight formed from the fp32 scale and rounded
+ *     once to dt; fp32 accumulation);
+ *   every other case: the general kernel (fp32 weights and products).
+ * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_UNSUPPORTED (bits, f32 dY),
+ * GPTQ_ERR_CUDA.  A bounded wait of the tensor-core kernel that gave up writes
+ * NaN over the CTA's outputs. */
+GPTQ_API gptq_status gptq_gemm_dgrad(const void* dY, gptq_dtype dt, int64_t m, int64_t n,
+                      int64_t lddy, const int32_t* qweight, const float* scales,
+                      const int32_t* zeros, const int32_t* g_idx, int64_t k, int bits,
+                      int group_size, int64_t ngroups, void* dX, int64_t lddx,
+                      gptq_stream_t stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *   V[t]   = scaling[a] * A_a x_t           (rank values, fp32)
+ *   out[t] = Y[t] + B_a V[t]                (summed in fp32, rounded once to dt)
+ * for every row t of request q, a = adapter[q].
+ *   Requests  starts int32[nreq + 1] (device), ascending: request q is the rows
+ *             [starts[q], starts[q + 1]) of the batch; lengths may be zero and
+ *             mixed.  adapter int32[nreq] (device): an index in [0, na), any
+ *             other value = no adapter.  Rows outside [starts[0], starts[nreq])
+ *             are left as they are in out and V.  Entries are clamped to
+ *             [0, m]; overlapping requests give unspecified rows, never an
+ *             access outside the batch.
+ *   Y        (m, n) dt or NULL (then out = B_a V); ldy >= n.  May be out itself
+ *            (with ldy == ldo); other overlaps of out with Y or X are rejected.
+ *            Rows of a request without an adapter get a copy of Y (0 if NULL).
+ *   X        (m, k) f16 or bf16 (dt), ldx >= k.
+ *   A        (na, rank, k) dt, B (na, n, rank) dt, contiguous; scaling fp32[na].
+ *   rank     a multiple of 8, 8 .. 128 (pad A and B with zeros).
+ *   out      (m, n) dt, ldo >= n.
+ *   V        (m, rank) fp32 out or NULL: what gptq_lora_backward needs (0 for rows
+ *            of a request without an adapter).
+ *   m < 2^27, nreq <= m + 65536.  The library allocates nothing; sums run in a fixed order.
+ * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_UNSUPPORTED (rank, f32),
+ * GPTQ_ERR_CUDA.  m == 0, n == 0, nreq == 0: no-op. */
+GPTQ_API gptq_status gptq_lora_add(const void* Y, int64_t ldy, const void* X, gptq_dtype dt,
+                      int64_t m, int64_t k, int64_t ldx, const void* A, const void* B,
+                      const float* scaling, int64_t na, int rank, const int32_t* starts,
+                      const int32_t* adapter, int64_t nreq, int64_t n, void* out, int64_t ldo,
+                      float* V, gptq_stream_t stream);
+
+/* Backward pass of gptq_lora_add:
+ *   U[t]   = scaling[a] * B_a^T dY[t]
+ *   out[t] = dX[t] + A_a^T U[t]
+ *   dA_a   = sum_t U[t] x_t^T,   dB_a = sum_t dY[t] V[t]^T   (t over a's rows)
+ * (the gradient that reaches Y is dY itself.)  Sums in fp32, rounded once.
+ *   dY       (m, n) dt, lddy >= n.
+ *   X        the forward pass's activations: (m, k) dt, ldx >= k, with x_scales
+ *            NULL; or the int8 codes of gptq_act_checkpoint (m, k) with x_scales
+ *            fp32 (m, ceil(k / 128)): then x_t is the restored row, in fp32.
+ *   V        (m, rank) fp32 from gptq_lora_add.
+ *   A, B, scaling, na, rank, starts, adapter, nreq  as in the forward pass.
+ *   dX       (m, k) dt or NULL (then out = A_a^T U), may be out itself; other
+ *            overlaps of out with dX or dY are rejected.
+ *   out      (m, k) dt, or NULL: no input gradient (the lowest layer); rows
+ *            outside the requests are left as they are.
+ *   dA       (na, rank, k), dB (na, n, rank) dt out, contiguous, written whole
+ *            (0 for an adapter without rows).
+ *   ws       GPTQ_OP_LORA_BACKWARD workspace.
+ * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_UNSUPPORTED (rank, f32),
+ * GPTQ_ERR_WORKSPACE, GPTQ_ERR_CUDA. */
+GPTQ_API gptq_status gptq_lora_backward(const void* dY, gptq_dtype dt, int64_t m, int64_t n,
+                      int64_t lddy, const void* X, int64_t ldx, const float* x_scales, int64_t k,
+                      const float* V, const void* A, const void* B, const float* scaling,
+                      int64_t na, int rank, const int32_t* starts, const int32_t* adapter,
+                      int64_t nreq, const void* dX, int64_t lddx, void* out, int64_t ldo,
+                      void* dA, void* dB, void* ws, size_t ws_bytes, gptq_stream_t stream);
+
+/* Activation checkpoint in 8 bits.  Each row is cut into blocks of 128 columns;
+ * per block, with top = max |x|:
+ *   scales = fl32(top / 127),  codes[c] = the integer nearest to
+ *   x[c] * fl32(127 / top), halves to even (taken from the exact product).
+ * A block whose top is below 2^-100 gets zeros; one that holds a NaN or an
+ * infinity gets the scale NaN (the whole block restores to NaN).
+ *   X       (m, k) dt (F32/F16/BF16), ldx >= k; any k.
+ *   codes   int8 (m, k) out, ldc >= k (in bytes).
+ *   scales  fp32 (m, ceil(k / 128)) out, contiguous.
+ * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_CUDA. */
+GPTQ_API gptq_status gptq_act_checkpoint(const void* X, gptq_dtype dt, int64_t m, int64_t k,
+                      int64_t ldx, int8_t* codes, int64_t ldc, float* scales,
+                      gptq_stream_t stream);
+
+/* The activations of a checkpoint: out[t, c] = codes[t, c] * scales[t, c / 128],
+ * formed in fp32 (at most the largest finite value for a finite scale) and
+ * rounded once to out_dt (F32/F16/BF16); ldo >= k.
+ * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_CUDA. */
+GPTQ_API gptq_status gptq_act_restore(const int8_t* codes, int64_t ldc, const float* scales,
+                      int64_t m, int64_t k, gptq_dtype out_dt, void* out, int64_t ldo,
+                      gptq_stream_t stream);
 
 /* Measured peak rates of the current device, for roofline fractions (a
  * calibration utility, not part of the method): fp32 FMA on the CUDA cores

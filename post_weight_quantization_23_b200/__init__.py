@@ -14,5 +14,6 @@ from ._lib import (  # noqa: F401
     LIB_PATH,
     load,
 )
-from .api import (GptqPlan, QuantConfig, hadamard_block, quant_matmul,  # noqa: F401
+from .api import (GptqPlan, QuantConfig, act_checkpoint, act_restore,  # noqa: F401
+                  hadamard_block, lora_add, lora_backward, quant_matmul, quant_matmul_dgrad,
                   quantize_layer, rotate, rotation_signs)

@@ -196,6 +196,103 @@ def quant_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
     return out
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the call runs on (the caching
+    allocator reuses its memory in that stream's order)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def quant_matmul_dgrad(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                       zeros: torch.Tensor, bits: int, group_size: int, k: int, g_idx=None,
+                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of quant_matmul with respect to its input, dX = dY W_hat, read
+    straight from the packed weights (gptq_gemm_dgrad): dY (m, n) f16/bf16 on the
+    device, the weights as for quant_matmul.  Returns dX (m, k) in dY's dtype
+    (``out`` if given)."""
+    if out is None:
+        out = _empty((dY.shape[0], k), dY.dtype, dY.device, stream)
+    _lib.gemm_dgrad(dY, qweight, scales, zeros, g_idx, bits, group_size, k, out, stream)
+    return out
+
+
+def lora_add(Y, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor,
+             starts: torch.Tensor, adapter: torch.Tensor, out: torch.Tensor | None = None,
+             V: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The low-rank adapters of many requests beside a shared projection
+    (gptq_lora_add): request q is the rows [starts[q], starts[q+1]) and uses
+    adapter[q] of A (na, rank, k), B (na, n, rank), scaling (na,); any index
+    outside [0, na) means none.
+
+        out[t] = Y[t] + B_a (scaling_a A_a x_t)
+
+    Without ``out`` Y (m, n) is updated in place; Y may be None when ``out`` is
+    given.  ``V`` (m, rank) fp32, if given, receives scaling_a A_a x_t, which
+    lora_backward needs.  Rows outside the requests are left as they are.
+    Returns the updated tensor."""
+    if out is None:
+        if Y is None:
+            raise GptqError(_lib.GPTQ_ERR_INVALID_ARG, "gptq_lora_add", "Y or out")
+        out = Y
+    _lib.lora_add(Y, X, A, B, scaling, starts, adapter, out, V, stream)
+    return out
+
+
+def lora_backward(dY: torch.Tensor, X: torch.Tensor, V: torch.Tensor, A: torch.Tensor,
+                  B: torch.Tensor, scaling: torch.Tensor, starts: torch.Tensor,
+                  adapter: torch.Tensor, dX: torch.Tensor | None,
+                  x_scales: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  dA: torch.Tensor | None = None, dB: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None, stream=None):
+    """Backward pass of lora_add (gptq_lora_backward).  X is the forward pass's
+    input, or the int8 codes of its act_checkpoint with ``x_scales``; V what
+    lora_add kept.  With U[t] = scaling_a B_a^T dY[t]:
+
+        out[t] = dX[t] + A_a^T U[t],  dA_a = sum_t U[t] x_t^T,  dB_a = sum_t dY[t] V[t]^T
+
+    Without ``out`` dX is updated in place; with neither, no input gradient is
+    formed.  ``ws`` is scratch memory of workspace_size(OP_LORA_BACKWARD, rank,
+    0, m) bytes, allocated here if not given.  Returns (out, dA, dB)."""
+    if out is None:
+        out = dX
+    if dA is None:
+        dA = _empty(A.shape, A.dtype, A.device, stream)
+    if dB is None:
+        dB = _empty(B.shape, B.dtype, B.device, stream)
+    if ws is None:
+        nbytes = _lib.workspace_size(_lib.OP_LORA_BACKWARD, A.shape[1], 0, dY.shape[0], None)
+        ws = _empty((max(nbytes, 1),), torch.uint8, dY.device, stream)
+    _lib.lora_backward(dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB, ws,
+                       stream)
+    return out, dA, dB
+
+
+def act_checkpoint(X: torch.Tensor, codes: torch.Tensor | None = None,
+                   scales: torch.Tensor | None = None, stream=None):
+    """Activations (m, k) f32/f16/bf16 kept in 8 bits for a backward pass
+    (gptq_act_checkpoint): int8 codes (m, k) and fp32 scales (m, ceil(k/128)),
+    one per row and block of 128 columns.  Returns (codes, scales)."""
+    m, k = X.shape
+    if codes is None:
+        codes = _empty((m, k), torch.int8, X.device, stream)
+    if scales is None:
+        scales = _empty((m, (k + 127) // 128), torch.float32, X.device, stream)
+    _lib.act_checkpoint(X, codes, scales, stream)
+    return codes, scales
+
+
+def act_restore(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float16,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The activations that act_checkpoint kept, codes * scales (gptq_act_restore),
+    in ``dtype`` (or into ``out``)."""
+    if out is None:
+        out = _empty(codes.shape, dtype, codes.device, stream)
+    _lib.act_restore(codes, scales, out, stream)
+    return out
+
+
 def hadamard_block(k: int, largest: int = 8192) -> int:
     """The largest power of two that divides k, at most ``largest`` (0 if
     below 256, which gptq_rotate does not take)."""

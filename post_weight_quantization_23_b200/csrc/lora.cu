@@ -1,0 +1,370 @@
+// The adapters of many requests beside a shared projection (gptq_lora_add):
+//   V[t] = scaling_a (A_a x_t),   out[t] = Y[t] + B_a V[t],
+// a = the adapter of the request that holds row t.  V stays in fp32; the sum
+// with Y is rounded once.
+//
+// Kernels:
+//   lora_decode_kernel   short requests and small batches: one launch, a cluster of
+//                        8 CTAs per piece of 8 rows of one request;
+//   lora_tc_kernel       (lora_tc.cu) long requests and the backward pass: the same
+//                        cluster on the 5th-generation tensor cores;
+//   lora_general_kernel  operands whose rows the wide loads cannot take.
+#include "lora.cuh"
+
+#include <algorithm>
+
+namespace gptq {
+
+bool lora_tc_supported(const LoraArgs& a);
+gptq_status lora_tc(const LoraArgs& a, bool bf16, bool backward, cudaStream_t s);
+
+namespace {
+
+// ---- general kernel ------------------------------------------------------------
+
+// One CTA per row, any alignment and strides.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+lora_general_kernel(LoraArgs a, int backward) {
+  using Ty = LoraType<BF16>;
+  using T = typename Ty::T;
+  __shared__ float v[LORA_MAX_RANK];
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int lo = 0, hi = a.nreq;  // the last request that starts at or before t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.starts[mid] <= t) lo = mid; else hi = mid;
+  }
+  if (t < a.starts[lo] || t >= a.starts[lo + 1]) return;
+  const int len = lora_clamp(a.starts[lo + 1], a.m) - lora_clamp(a.starts[lo], a.m);
+  if (len < a.min_len || len > a.max_len) return;
+  const int ad = a.adapter[lo];
+  const bool none = ad < 0 || ad >= a.na;
+  const T* x = (const T*)a.X + (int64_t)t * a.ldx;
+  const T* P = (const T*)a.P + (none ? 0 : (int64_t)ad * a.r * a.K);
+  const T* Q = (const T*)a.Q + (none ? 0 : (int64_t)ad * a.r * a.N);
+  const int64_t prs = backward ? 1 : a.K, pcs = backward ? a.r : 1;
+  const int64_t qrs = backward ? a.N : 1, qcs = backward ? 1 : a.r;
+  const float sc = none ? 0.f : a.scaling[ad];
+  for (int p = warp; p < a.r; p += 8) {
+    float s = 0.f;
+    if (!none)
+      for (int c = lane; c < a.K; c += 32) s = fmaf(to_f32(x[c]), to_f32(P[p * prs + c * pcs]), s);
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) {
+      v[p] = none ? 0.f : s * sc;
+      if (a.V != nullptr) a.V[(int64_t)t * a.r + p] = v[p];
+    }
+  }
+  __syncthreads();
+  if (a.out == nullptr) return;
+  const T* y = (const T*)a.Y + (int64_t)t * a.ldy;
+  T* o = (T*)a.out + (int64_t)t * a.ldo;
+  if (none) {
+    if (a.Y != a.out)
+      for (int j = threadIdx.x; j < a.N; j += 256) o[j] = a.Y != nullptr ? y[j] : Ty::cvt(0.f);
+    return;
+  }
+  for (int j = threadIdx.x; j < a.N; j += 256) {
+    float s = 0.f;
+    for (int p = 0; p < a.r; ++p) s = fmaf(v[p], to_f32(Q[p * qrs + j * qcs]), s);
+    o[j] = Ty::cvt(a.Y != nullptr ? to_f32(y[j]) + s : s);
+  }
+}
+
+// ---- decode kernel --------------------------------------------------------------
+
+constexpr int LD_THREADS = 256;
+constexpr int LD_WARPS = LD_THREADS / 32;
+constexpr int LD_TT = 8;  // rows per piece: the n of mma.sync m16n8k16
+
+template <bool BF16>
+__device__ __forceinline__ void ld_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ld_nc_u4(const void* p) {
+  return __ldg(reinterpret_cast<const uint4*>(p));
+}
+
+// A cluster of 8 CTAs takes one piece: up to 8 rows of one request.  The
+// adapter's matrices are what it has to read ((k + n) r elements, the rows are
+// few), so both products take them straight from global memory as the 16-row
+// operand of mma.sync m16n8k16 with the 8 tokens as its columns: the order of a
+// reduction is free, so lane (g, t) takes 8 consecutive columns of row g in one
+// 16-byte load where the fragment layout would want four 4-byte ones, and the
+// activations' fragments take the same columns in the same lanes.
+//   1. V^T = A x: the cluster's 64 warps share the columns in runs of 64; the
+//      warps of a CTA add up in shared memory, and each CTA hands its sums to all
+//      eight through distributed shared memory (one cluster barrier).
+//   2. out^T = B V: the 64 warps share the n output rows, 16 at a time; V is the
+//      other operand, each value as hi + lo of the 16-bit type (f16: each row
+//      first scaled by a power of two, so that neither leaves the type's range).
+// The first tile of B is requested before the barrier.  One launch, no workspace,
+// sums in a fixed order.
+template <bool BF16, int RP>
+__global__ void __launch_bounds__(LD_THREADS)
+lora_decode_kernel(LoraArgs a, int yvec) {
+  using Ty = LoraType<BF16>;
+  using T = typename Ty::T;
+  constexpr int MT = RP / 16;                  // 16-row tiles of the rank
+  constexpr int KC = RP >= 32 ? RP / 32 : 1;   // 32-wide chunks of the rank in product 2
+  constexpr int NS = RP >= 32 ? 2 : 1;         // 16-wide steps per chunk
+  extern __shared__ __align__(16) float ld_smem[];
+  constexpr int PS = RP * LD_TT;               // values of one partial sum
+  float* red = ld_smem;                        // [LD_WARPS][PS] per-warp sums, then V
+  float* part = ld_smem + LD_WARPS * PS;       // [LORA_CLUSTER][PS] one slot per CTA
+  __shared__ float fac[LD_TT];
+  __shared__ int scan[LD_THREADS / 32 + 3];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = (int)cluster_rank();
+  pdl_wait();
+  pdl_trigger();
+  const LoraPiece pc =
+      lora_find_piece<LD_THREADS>(a.starts, a.adapter, a.nreq, a.m, a.na, LD_TT, a.min_len,
+                                  a.max_len, (int)blockIdx.x / LORA_CLUSTER, scan);
+  if (pc.cnt == 0) return;  // the same for the whole cluster
+  const T* Y = (const T*)a.Y;
+  T* out = (T*)a.out;
+  const int gw = rank * LD_WARPS + warp;
+  constexpr int NW = LORA_CLUSTER * LD_WARPS;
+  if (pc.a < 0) {
+    for (int i = 0; i < pc.cnt; ++i) {
+      const int64_t row = pc.t0 + i;
+      if (a.Y != a.out)
+        for (int j = rank * LD_THREADS + tid; j < a.N; j += LORA_CLUSTER * LD_THREADS)
+          out[row * a.ldo + j] = a.Y != nullptr ? Y[row * a.ldy + j] : Ty::cvt(0.f);
+      if (a.V != nullptr && rank == 0)
+        for (int p = tid; p < a.r; p += LD_THREADS) a.V[row * a.r + p] = 0.f;
+    }
+    return;
+  }
+  cluster_arrive();  // this CTA runs: peers may write to its shared memory
+  const T* A = (const T*)a.P + (int64_t)pc.a * a.r * a.K;
+  const T* B = (const T*)a.Q + (int64_t)pc.a * a.r * a.N;
+  const bool tok = g < pc.cnt;
+  const T* xrow = (const T*)a.X + (int64_t)(pc.t0 + (tok ? g : 0)) * a.ldx;
+
+  // 1. per-warp sums of A x over this warp's columns
+  float acc[MT][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+  const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+  for (int c0 = gw * 64; c0 < a.K; c0 += NW * 64) {
+    const int ca = c0 + 8 * t, cb = ca + 32;
+    const bool oka = ca < a.K, okb = cb < a.K;
+    const uint4 xa = tok && oka ? ld_nc_u4(xrow + ca) : zero4;
+    const uint4 xb = tok && okb ? ld_nc_u4(xrow + cb) : zero4;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int p0 = 16 * i + g, p1 = p0 + 8;
+      const T* r0 = A + (int64_t)p0 * a.K;
+      const T* r1 = A + (int64_t)p1 * a.K;
+      const uint4 a0 = p0 < a.r && oka ? ld_nc_u4(r0 + ca) : zero4;
+      const uint4 a1 = p1 < a.r && oka ? ld_nc_u4(r1 + ca) : zero4;
+      const uint4 b0 = p0 < a.r && okb ? ld_nc_u4(r0 + cb) : zero4;
+      const uint4 b1 = p1 < a.r && okb ? ld_nc_u4(r1 + cb) : zero4;
+      ld_mma<BF16>(acc[i], a0.x, a1.x, a0.y, a1.y, xa.x, xa.y);
+      ld_mma<BF16>(acc[i], a0.z, a1.z, a0.w, a1.w, xa.z, xa.w);
+      ld_mma<BF16>(acc[i], b0.x, b1.x, b0.y, b1.y, xb.x, xb.y);
+      ld_mma<BF16>(acc[i], b0.z, b1.z, b0.w, b1.w, xb.z, xb.w);
+    }
+  }
+  // the first tile of B (rows j of this warp, the lane's columns of the rank)
+  uint4 w0[KC], w1[KC];
+  auto load_b = [&](int j0) {
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const int p = RP >= 32 ? 32 * c + 8 * t : 4 * t;
+      const bool ok0 = p < a.r && j0 + g < a.N, ok1 = p < a.r && j0 + g + 8 < a.N;
+      const T* q0 = B + (int64_t)(j0 + g) * a.r + p;
+      const T* q1 = q0 + (int64_t)8 * a.r;
+      if (RP >= 32) {
+        w0[c] = ok0 ? ld_nc_u4(q0) : zero4;
+        w1[c] = ok1 ? ld_nc_u4(q1) : zero4;
+      } else {
+        const uint2 u0 = ok0 ? __ldg((const uint2*)q0) : make_uint2(0u, 0u);
+        const uint2 u1 = ok1 ? __ldg((const uint2*)q1) : make_uint2(0u, 0u);
+        w0[c] = make_uint4(u0.x, u0.y, 0u, 0u);
+        w1[c] = make_uint4(u1.x, u1.y, 0u, 0u);
+      }
+    }
+  };
+  if (a.out != nullptr) load_b(gw * 16);
+  // lane (g, t) holds (rank row 16 i + g | + 8, token 2 t | + 1); laid out by token
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    float* rw = red + warp * PS + 16 * i + g;
+    rw[(2 * t) * RP] = acc[i][0];
+    rw[(2 * t + 1) * RP] = acc[i][1];
+    rw[(2 * t) * RP + 8] = acc[i][2];
+    rw[(2 * t + 1) * RP + 8] = acc[i][3];
+  }
+  __syncthreads();
+  cluster_wait();
+  for (int e = tid; e < PS / 4; e += LD_THREADS) {
+    float4 s = reinterpret_cast<const float4*>(red)[e];
+#pragma unroll
+    for (int w = 1; w < LD_WARPS; ++w) {
+      const float4 v = reinterpret_cast<const float4*>(red + w * PS)[e];
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(part + rank * PS + 4 * e);
+#pragma unroll
+    for (int c = 0; c < LORA_CLUSTER; ++c) cluster_st_f4(cluster_map(dst, c), s);
+  }
+  cluster_arrive();
+  cluster_wait();
+  const float sc = a.scaling[pc.a];
+  float* vs = red;  // V of the piece, [token][RP]
+  for (int e = tid; e < PS; e += LD_THREADS) {
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < LORA_CLUSTER; ++c) s += part[c * PS + e];
+    s *= sc;
+    vs[e] = s;
+    const int tk = e / RP, p = e % RP;
+    if (a.V != nullptr && rank == 0 && tk < pc.cnt && p < a.r)
+      a.V[(int64_t)(pc.t0 + tk) * a.r + p] = s;
+  }
+  __syncthreads();
+  if (a.out == nullptr) return;
+  if (!BF16) {
+    float top = 0.f;
+    for (int p = lane; p < RP; p += 32) top = fmaxf(top, fabsf(vs[warp * RP + p]));
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) fac[warp] = lora_row_factor(top);
+    __syncthreads();
+  }
+  uint32_t vh[KC * NS][2], vl[KC * NS][2];
+  {
+    const float f = BF16 ? 1.f : fac[g];
+    const float* vr = vs + g * RP;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int h = 0; h < NS; ++h) {
+        const int p = RP >= 32 ? 32 * c + 8 * t + 4 * h : 4 * t;
+        const float4 v = *reinterpret_cast<const float4*>(vr + p);
+        lora_split<BF16>(v.x * f, v.y * f, vh[c * NS + h][0], vl[c * NS + h][0]);
+        lora_split<BF16>(v.z * f, v.w * f, vh[c * NS + h][1], vl[c * NS + h][1]);
+      }
+  }
+  __syncthreads();  // red is reused as the warps' transposing buffers
+  float* tile = red + warp * (LD_TT * 20);  // [token][16 + 4]
+  const float if0 = BF16 ? 1.f : __fdiv_rn(1.f, fac[2 * t]);       // powers of two: exact
+  const float if1 = BF16 ? 1.f : __fdiv_rn(1.f, fac[2 * t + 1]);
+  for (int j0 = gw * 16; j0 < a.N; j0 += NW * 16) {
+    if (j0 != gw * 16) load_b(j0);
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      ld_mma<BF16>(d, w0[c].x, w1[c].x, w0[c].y, w1[c].y, vl[c * NS][0], vl[c * NS][1]);
+      ld_mma<BF16>(d, w0[c].x, w1[c].x, w0[c].y, w1[c].y, vh[c * NS][0], vh[c * NS][1]);
+      if (NS == 2) {
+        ld_mma<BF16>(d, w0[c].z, w1[c].z, w0[c].w, w1[c].w, vl[c * NS + NS - 1][0],
+                     vl[c * NS + NS - 1][1]);
+        ld_mma<BF16>(d, w0[c].z, w1[c].z, w0[c].w, w1[c].w, vh[c * NS + NS - 1][0],
+                     vh[c * NS + NS - 1][1]);
+      }
+    }
+    tile[(2 * t) * 20 + g] = d[0] * if0;
+    tile[(2 * t + 1) * 20 + g] = d[1] * if1;
+    tile[(2 * t) * 20 + g + 8] = d[2] * if0;
+    tile[(2 * t + 1) * 20 + g + 8] = d[3] * if1;
+    __syncwarp();
+    // lane = (token g, four output columns 4 t)
+    const int j = j0 + 4 * t;
+    if (tok && j < a.N) {
+      const float4 v = *reinterpret_cast<const float4*>(tile + g * 20 + 4 * t);
+      const int64_t row = pc.t0 + g;
+      const T* yp = Y + row * a.ldy + j;
+      T* op = out + row * a.ldo + j;
+      if (yvec && j + 4 <= a.N) {
+        float2 y0 = make_float2(0.f, 0.f), y1 = y0;
+        if (a.Y != nullptr) {
+          const uint2 u = *reinterpret_cast<const uint2*>(yp);
+          y0 = Ty::unpack(u.x), y1 = Ty::unpack(u.y);
+        }
+        *reinterpret_cast<uint2*>(op) =
+            make_uint2(Ty::pack(y0.x + v.x, y0.y + v.y), Ty::pack(y1.x + v.z, y1.y + v.w));
+      } else {
+        const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j + i < a.N) op[i] = Ty::cvt((a.Y != nullptr ? to_f32(yp[i]) : 0.f) + e[i]);
+      }
+    }
+    __syncwarp();
+  }
+}
+
+template <bool BF16, int RP>
+gptq_status launch_decode(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
+  const int yvec = (uintptr_t)a.Y % 8 == 0 && (uintptr_t)a.out % 8 == 0 &&
+                   (a.Y == nullptr || a.ldy % 4 == 0) && a.ldo % 4 == 0;
+  constexpr size_t smem = sizeof(float) * (LD_WARPS + LORA_CLUSTER) * RP * LD_TT;
+  static_assert((LD_WARPS + LORA_CLUSTER) * RP * LD_TT >= LD_WARPS * LD_TT * 20, "transposing buffers fit");
+  if (smem_optin((const void*)lora_decode_kernel<BF16, RP>, smem) != cudaSuccess)
+    return GPTQ_ERR_CUDA;
+  launch_cluster_pdl(lora_decode_kernel<BF16, RP>, dim3((unsigned)(pieces * LORA_CLUSTER)),
+                     dim3(LD_THREADS), smem, LORA_CLUSTER, s, a, yvec);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+template <bool BF16>
+gptq_status decode_ranks(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
+  if (a.r <= 16) return launch_decode<BF16, 16>(a, pieces, s);
+  if (a.r <= 32) return launch_decode<BF16, 32>(a, pieces, s);
+  if (a.r <= 64) return launch_decode<BF16, 64>(a, pieces, s);
+  return launch_decode<BF16, 128>(a, pieces, s);
+}
+
+bool rows16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
+
+gptq_status lora_general(const LoraArgs& a, bool bf16, bool backward, cudaStream_t s) {
+  if (bf16)
+    launch_pdl(lora_general_kernel<true>, dim3((unsigned)a.m), dim3(256), 0, s, a, (int)backward);
+  else
+    launch_pdl(lora_general_kernel<false>, dim3((unsigned)a.m), dim3(256), 0, s, a, (int)backward);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
+  a.min_len = 1;
+  a.max_len = a.m;
+  // the decode kernel reads rows of X, A and B in 16-byte pieces
+  if (!rows16(a.X, a.ldx) || !rows16(a.P, a.K) || !rows16(a.Q, a.r))
+    return lora_general(a, bf16, false, s);
+  const int64_t pieces = std::min<int64_t>(a.m, (int64_t)a.m / LD_TT + a.nreq);
+  return bf16 ? decode_ranks<true>(a, pieces, s) : decode_ranks<false>(a, pieces, s);
+}
+
+gptq_status lora_low_impl(LoraArgs a, bool bf16, cudaStream_t s) {
+  a.min_len = 1;
+  a.max_len = a.m;
+  return lora_general(a, bf16, true, s);
+}
+
+}  // namespace gptq

@@ -1,0 +1,203 @@
+// Shared pieces of the adapter kernels (lora.cu, lora_tc.cu, lora_grad.cu).
+//
+// Requests are rows [starts[q], starts[q + 1]) of the batch, each with one
+// adapter (an index outside [0, na) means none).  The kernels never trust the
+// device arrays: starts are clamped to [0, m], a request whose end is not above
+// its start is empty, so no access leaves the batch whatever they hold.
+#pragma once
+
+#include "common.cuh"
+
+namespace gptq {
+
+constexpr int LORA_MAX_RANK = 128;
+constexpr int LORA_CLUSTER = 8;  // CTAs that share one piece of a request
+
+struct LoraPiece {
+  int t0 = 0;    // first row
+  int cnt = 0;   // rows (0: no such piece)
+  int a = -1;    // adapter, -1 = none
+};
+
+__device__ __forceinline__ int lora_clamp(int v, int m) { return min(max(v, 0), m); }
+
+// Pieces of TT rows of one request that this launch takes (lengths in
+// [min_len, max_len]).
+__device__ __forceinline__ int lora_pieces(const int32_t* starts, int q, int m, int TT, int min_len,
+                                           int max_len) {
+  const int len = lora_clamp(starts[q + 1], m) - lora_clamp(starts[q], m);
+  return (len < min_len || len > max_len || len <= 0) ? 0 : (len + TT - 1) / TT;
+}
+
+// The `piece`-th piece over all requests, found by the whole CTA (NT threads, a
+// power of two of at least 32): each thread counts the pieces of a run of
+// requests, a scan over the threads locates the run, its thread walks it.
+// `sm` holds NT / 32 + 3 ints.
+template <int NT>
+__device__ __forceinline__ LoraPiece lora_find_piece(const int32_t* __restrict__ starts,
+                                                     const int32_t* __restrict__ adapter, int nreq,
+                                                     int m, int na, int TT, int min_len,
+                                                     int max_len, int piece, int* sm) {
+  LoraPiece r;
+  if (nreq == 1) {
+    const int b = lora_clamp(starts[0], m), e = lora_clamp(starts[1], m);
+    if (piece < lora_pieces(starts, 0, m, TT, min_len, max_len)) {
+      r.t0 = b + piece * TT;
+      r.cnt = min(TT, e - r.t0);
+      r.a = adapter[0];
+    }
+  } else {
+    int* found = sm + NT / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (nreq + NT - 1) / NT;
+    const int q0 = min(nreq, tid * per), q1 = min(nreq, q0 + per);
+    int own = 0;
+    for (int q = q0; q < q1; ++q) own += lora_pieces(starts, q, m, TT, min_len, max_len);
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sm[warp] = inc;
+    if (tid == 0) found[1] = 0;
+    __syncthreads();
+    int before = inc - own;
+    for (int w = 0; w < warp; ++w) before += sm[w];
+    if (piece >= before && piece < before + own) {  // at most one thread
+      int left = piece - before, q = q0;
+      for (; q < q1; ++q) {
+        const int p = lora_pieces(starts, q, m, TT, min_len, max_len);
+        if (left < p) break;
+        left -= p;
+      }
+      const int t0 = lora_clamp(starts[q], m) + left * TT;
+      found[0] = t0;
+      found[1] = min(TT, lora_clamp(starts[q + 1], m) - t0);
+      found[2] = adapter[q];
+    }
+    __syncthreads();
+    r.t0 = found[0];
+    r.cnt = found[1];
+    r.a = r.cnt > 0 ? found[2] : -1;
+    __syncthreads();  // sm may be reused
+  }
+  if (r.a < 0 || r.a >= na) r.a = -1;
+  return r;
+}
+
+// ---- clusters ----------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The address, in CTA `rank`'s shared memory, of this CTA's shared address.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_st_f4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
+}
+// All threads of all CTAs of the cluster; writes before it are seen after it.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                      int cluster, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// ---- 16-bit types ------------------------------------------------------------
+
+template <bool BF16> struct LoraType;
+template <> struct LoraType<false> {
+  using T = __half;
+  __device__ static T cvt(float v) { return __float2half_rn(v); }
+  __device__ static uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __device__ static float2 unpack(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  }
+};
+template <> struct LoraType<true> {
+  using T = __nv_bfloat16;
+  __device__ static T cvt(float v) { return __float2bfloat16_rn(v); }
+  __device__ static uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __device__ static float2 unpack(uint32_t u) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+  }
+};
+
+// Two 32-bit values as the sum of two 16-bit pairs, hi + lo (2 x 8 significant
+// bits for bf16, 2 x 11 for f16).  A value whose hi part is not finite has no lo.
+template <bool BF16>
+__device__ __forceinline__ void lora_split(float a, float b, uint32_t& hi, uint32_t& lo) {
+  using Ty = LoraType<BF16>;
+  hi = Ty::pack(a, b);
+  const float2 h = Ty::unpack(hi);
+  const float la = isfinite(h.x) ? a - h.x : 0.f, lb = isfinite(h.y) ? b - h.y : 0.f;
+  lo = Ty::pack(la, lb);
+}
+
+// f16 only: the power of two that brings a row whose largest magnitude is `top`
+// to [2^7, 2^8), where neither half of the split leaves f16's range; 1 for a
+// zero or non-finite row.  Exact to apply and to take back.
+__device__ __forceinline__ float lora_row_factor(float top) {
+  if (!(top > 0.f) || !isfinite(top)) return 1.f;
+  int e = (int)((__float_as_uint(top) >> 23) & 0xFFu) - 127;
+  e = min(max(e, -100), 120);
+  return __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+}
+
+// The arguments that the adapter kernels share.  Forward (add): reduction over
+// K = k with P = A (na, r, k), output over N = n with Q = B (na, n, r).
+// Backward: K = n with P = B, N = k with Q = A.
+struct LoraArgs {
+  const void* X;  // (m, K) the rows that are reduced
+  int64_t ldx;
+  const void* P;
+  const void* Q;
+  const float* scaling;
+  const int32_t* starts;
+  const int32_t* adapter;
+  const void* Y;  // (m, N) added to, or NULL
+  int64_t ldy;
+  void* out;      // (m, N), or NULL: V alone
+  int64_t ldo;
+  float* V;       // (m, r) or NULL
+  int m, K, N, r, na, nreq;
+  int min_len, max_len;  // request lengths that this launch takes
+  uint32_t spin;
+};
+
+}  // namespace gptq
