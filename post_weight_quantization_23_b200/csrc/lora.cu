@@ -15,7 +15,7 @@
 
 namespace gptq {
 
-bool lora_tc_supported(const LoraArgs& a);
+bool lora_tc_supported(const LoraArgs& a, bool backward);
 gptq_status lora_tc(const LoraArgs& a, bool bf16, bool backward, cudaStream_t s);
 
 namespace {
@@ -351,19 +351,36 @@ gptq_status lora_general(const LoraArgs& a, bool bf16, bool backward, cudaStream
 
 }  // namespace
 
+// Batches of up to this many rows go to the decode kernel whole; in larger ones it
+// takes the requests of up to LORA_SHORT rows.
+constexpr int LORA_DECODE_ROWS = 256;
+constexpr int LORA_SHORT = 24;
+
 gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
   a.min_len = 1;
   a.max_len = a.m;
   // the decode kernel reads rows of X, A and B in 16-byte pieces
   if (!rows16(a.X, a.ldx) || !rows16(a.P, a.K) || !rows16(a.Q, a.r))
     return lora_general(a, bf16, false, s);
-  const int64_t pieces = std::min<int64_t>(a.m, (int64_t)a.m / LD_TT + a.nreq);
-  return bf16 ? decode_ranks<true>(a, pieces, s) : decode_ranks<false>(a, pieces, s);
+  const bool tc = a.m > LORA_DECODE_ROWS && lora_tc_supported(a, false);
+  if (!tc || a.nreq > 1) {
+    if (tc) a.max_len = LORA_SHORT;
+    const int64_t pieces = std::min<int64_t>(
+        std::min<int64_t>(a.m, (int64_t)a.m / LD_TT + a.nreq), a.nreq * cdiv(a.max_len, LD_TT));
+    const gptq_status st =
+        bf16 ? decode_ranks<true>(a, pieces, s) : decode_ranks<false>(a, pieces, s);
+    if (st != GPTQ_OK || !tc) return st;
+    a.min_len = LORA_SHORT + 1;
+    a.max_len = a.m;
+  }
+  return lora_tc(a, bf16, false, s);
 }
 
+// U = scaling B^T dY and, where a.out is set, out = Y + A^T U.
 gptq_status lora_low_impl(LoraArgs a, bool bf16, cudaStream_t s) {
   a.min_len = 1;
   a.max_len = a.m;
+  if (lora_tc_supported(a, true)) return lora_tc(a, bf16, true, s);
   return lora_general(a, bf16, true, s);
 }
 

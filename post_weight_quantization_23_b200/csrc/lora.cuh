@@ -30,7 +30,7 @@ __device__ __forceinline__ int lora_pieces(const int32_t* starts, int q, int m, 
 }
 
 // The `piece`-th piece over all requests, found by the whole CTA (NT threads, a
-// power of two of at least 32): each thread counts the pieces of a run of
+// multiple of 32): each thread counts the pieces of a run of
 // requests, a scan over the threads locates the run, its thread walks it.
 // `sm` holds NT / 32 + 3 ints.
 template <int NT>
@@ -106,10 +106,34 @@ __device__ __forceinline__ void cluster_st_f4(uint32_t addr, float4 v) {
 }
 // All threads of all CTAs of the cluster; writes before it are seen after it.
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Arrive on the mbarrier at `addr` (an address of cluster_map): this thread's
+// writes, those to other CTAs included, are seen by whoever acquires the phase.
+__device__ __forceinline__ void cluster_mbar_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// tc::mbar_wait_warp for a phase that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool cluster_mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                                       volatile int* abort_flag, uint32_t limit) {
+  const uint32_t a = (uint32_t)__cvta_generic_to_shared(bar);
+  uint32_t ok = 0;
+  for (uint32_t i = 0; i < limit && !ok; ++i) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if ((i & 1023u) == 1023u && *abort_flag) break;
+  }
+  if (!ok) *abort_flag = 1;
+  return __all_sync(0xffffffffu, ok != 0);
 }
 
 template <typename... KArgs, typename... Args>
