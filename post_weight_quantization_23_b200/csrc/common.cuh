@@ -56,6 +56,9 @@ EncodeTiledFn tensormap_encoder();
 // Opt the kernel `func` into `bytes` of dynamic shared memory on the current
 // device (once per device and size; the error of a failed opt-in is returned).
 cudaError_t smem_optin(const void* func, size_t bytes);
+// Clusters of `cluster` CTAs of the kernel that fit the current device at once
+// (asked once per device and kernel; at least 1).
+int resident_clusters(const void* func, int cluster, int threads, size_t smem);
 // SM count of the current device.
 int sm_count();
 // Polls after which a pipeline wait of a tensor-core kernel gives up

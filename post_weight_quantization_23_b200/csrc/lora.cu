@@ -144,14 +144,7 @@ lora_decode_kernel(LoraArgs a, int yvec) {
   const int gw = rank * LD_WARPS + warp;
   constexpr int NW = LORA_CLUSTER * LD_WARPS;
   if (pc.a < 0) {
-    for (int i = 0; i < pc.cnt; ++i) {
-      const int64_t row = pc.t0 + i;
-      if (a.Y != a.out)
-        for (int j = rank * LD_THREADS + tid; j < a.N; j += LORA_CLUSTER * LD_THREADS)
-          out[row * a.ldo + j] = a.Y != nullptr ? Y[row * a.ldy + j] : Ty::cvt(0.f);
-      if (a.V != nullptr && rank == 0)
-        for (int p = tid; p < a.r; p += LD_THREADS) a.V[row * a.r + p] = 0.f;
-    }
+    lora_copy_piece<T>(a, pc, rank, LORA_CLUSTER, LD_THREADS, yvec == 2);
     return;
   }
   cluster_arrive();  // this CTA runs: peers may write to its shared memory
@@ -318,8 +311,12 @@ lora_decode_kernel(LoraArgs a, int yvec) {
 
 template <bool BF16, int RP>
 gptq_status launch_decode(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
-  const int yvec = (uintptr_t)a.Y % 8 == 0 && (uintptr_t)a.out % 8 == 0 &&
-                   (a.Y == nullptr || a.ldy % 4 == 0) && a.ldo % 4 == 0;
+  // rows of Y and out on 16-byte (2) or 8-byte (1) boundaries
+  auto on = [&](int bytes) {
+    return (uintptr_t)a.Y % bytes == 0 && (uintptr_t)a.out % bytes == 0 &&
+           (a.Y == nullptr || a.ldy * 2 % bytes == 0) && a.ldo * 2 % bytes == 0;
+  };
+  const int yvec = on(16) ? 2 : on(8) ? 1 : 0;
   constexpr size_t smem = sizeof(float) * (LD_WARPS + LORA_CLUSTER) * RP * LD_TT;
   static_assert((LD_WARPS + LORA_CLUSTER) * RP * LD_TT >= LD_WARPS * LD_TT * 20, "transposing buffers fit");
   if (smem_optin((const void*)lora_decode_kernel<BF16, RP>, smem) != cudaSuccess)

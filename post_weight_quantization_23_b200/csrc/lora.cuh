@@ -104,6 +104,9 @@ __device__ __forceinline__ void cluster_st_f4(uint32_t addr, float4 v) {
                "f"(v.z), "f"(v.w)
                : "memory");
 }
+__device__ __forceinline__ void cluster_st_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // All threads of all CTAs of the cluster; writes before it are seen after it.
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -223,5 +226,86 @@ struct LoraArgs {
   int min_len, max_len;  // request lengths that this launch takes
   uint32_t spin;
 };
+
+// Pieces first, first + stride, .. (at most `cap`, from the `skip`-th of them) of
+// TT rows, into `table`, by the whole CTA; their number.  Each thread counts the
+// pieces of a run of requests, a scan locates them, and each thread writes those
+// of its run that are asked for.  `sm` holds NT / 32 + 1 ints.
+template <int NT>
+__device__ __forceinline__ int lora_find_pieces(const LoraArgs& a, int TT, int first, int stride,
+                                                int skip, LoraPiece* table, int cap, int* sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.nreq + NT - 1) / NT;
+  const int q0 = min(a.nreq, tid * per), q1 = min(a.nreq, q0 + per);
+  int own = 0;
+  for (int q = q0; q < q1; ++q) own += lora_pieces(a.starts, q, a.m, TT, a.min_len, a.max_len);
+  int inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  __syncthreads();  // the last use of sm and table is over
+  if (lane == 31) sm[warp] = inc;
+  __syncthreads();
+  int at = inc - own, total = 0;  // pieces before this thread's run, of all
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) at += sm[w];
+    total += sm[w];
+  }
+  // the i-th entry is piece first + (skip + i) * stride
+  const int64_t p0 = first + (int64_t)skip * stride;
+  const int64_t n = total > p0 ? min((int64_t)cap, (total - p0 + stride - 1) / stride) : 0;
+  for (int q = q0; q < q1; ++q) {
+    const int c = lora_pieces(a.starts, q, a.m, TT, a.min_len, a.max_len);
+    if (c > 0) {
+      int64_t i = at <= p0 ? 0 : (at - p0 + stride - 1) / stride;
+      for (; i < n && p0 + i * stride < at + c; ++i) {
+        LoraPiece r;
+        r.t0 = lora_clamp(a.starts[q], a.m) + (int)(p0 + i * stride - at) * TT;
+        r.cnt = min(TT, lora_clamp(a.starts[q + 1], a.m) - r.t0);
+        const int ad = a.adapter[q];
+        r.a = ad < 0 || ad >= a.na ? -1 : ad;
+        table[i] = r;
+      }
+    }
+    at += c;
+  }
+  __syncthreads();
+  return (int)n;
+}
+
+// The rows of a request without an adapter: out = Y (0 without Y) unless they are
+// the same, V = 0.  CTA `rank` of `nctas` takes every nctas-th 64-column run of all
+// rows; `vec`: rows of Y and out start on 16-byte boundaries.
+template <typename T>
+__device__ __forceinline__ void lora_copy_piece(const LoraArgs& a, const LoraPiece& pc, int rank,
+                                                int nctas, int nthreads, int vec) {
+  const T* Y = (const T*)a.Y;
+  T* out = (T*)a.out;
+  if (out != nullptr && a.Y != a.out) {
+    const int runs = (a.N + 63) / 64;
+    const int mine = runs <= rank ? 0 : (runs - rank + nctas - 1) / nctas;
+    const int total = pc.cnt * mine * 8;  // vectors of 8 values
+#pragma unroll 4
+    for (int e = threadIdx.x; e < total; e += nthreads) {
+      const int v = e % 8, run = (e / 8) % mine, i = e / (8 * mine);
+      const int j = (rank + nctas * run) * 64 + 8 * v;
+      const int64_t row = pc.t0 + i;
+      const T* y = Y + row * a.ldy + j;
+      T* o = out + row * a.ldo + j;
+      if (vec && j + 8 <= a.N) {
+        *reinterpret_cast<uint4*>(o) =
+            Y != nullptr ? *reinterpret_cast<const uint4*>(y) : make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        for (int q = 0; q < 8 && j + q < a.N; ++q)
+          reinterpret_cast<unsigned short*>(o)[q] =
+              Y != nullptr ? reinterpret_cast<const unsigned short*>(y)[q] : (unsigned short)0;
+      }
+    }
+  }
+  if (a.V != nullptr && rank == 0)
+    for (int e = threadIdx.x; e < pc.cnt * a.r; e += nthreads) a.V[(int64_t)pc.t0 * a.r + e] = 0.f;
+}
 
 }  // namespace gptq

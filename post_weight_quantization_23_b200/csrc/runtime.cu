@@ -47,6 +47,33 @@ cudaError_t smem_optin(const void* func, size_t bytes) {
   return e;
 }
 
+int resident_clusters(const void* func, int cluster, int threads, size_t smem) {
+  static std::map<std::pair<int, const void*>, int> known;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  std::lock_guard<std::mutex> lock(g_optin_mu);
+  int& n = known[std::make_pair(dev, func)];
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int got = 0;
+  if (cudaOccupancyMaxActiveClusters(&got, func, &cfg) != cudaSuccess || got < 1) {
+    (void)cudaGetLastError();
+    return 1;
+  }
+  n = got;
+  return n;
+}
+
 int sm_count() {
   int dev = 0, nsm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
