@@ -159,6 +159,12 @@ inline cudaError_t launch_cluster_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+__device__ __forceinline__ float cluster_ld_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // ---- 16-bit types ------------------------------------------------------------
 
 template <bool BF16> struct LoraType;
@@ -206,39 +212,50 @@ __device__ __forceinline__ float lora_row_factor(float top) {
   return __uint_as_float((uint32_t)(127 + 7 - e) << 23);
 }
 
-// The arguments that the adapter kernels share.  Forward (add): reduction over
+// The requests of a batch, and the arguments that the adapter kernels share.  Forward (add): reduction over
 // K = k with P = A (na, r, k), output over N = n with Q = B (na, n, r).
 // Backward: K = n with P = B, N = k with Q = A.
-struct LoraArgs {
+struct LoraRequests {
+  const int32_t* starts;
+  const int32_t* adapter;
+  int m, na, nreq;
+  int min_len, max_len;  // request lengths that this launch takes
+};
+
+struct LoraArgs : LoraRequests {
   const void* X;  // (m, K) the rows that are reduced
   int64_t ldx;
   const void* P;
   const void* Q;
   const float* scaling;
-  const int32_t* starts;
-  const int32_t* adapter;
   const void* Y;  // (m, N) added to, or NULL
   int64_t ldy;
   void* out;      // (m, N), or NULL: V alone
   int64_t ldo;
   float* V;       // (m, r) or NULL
-  int m, K, N, r, na, nreq;
-  int min_len, max_len;  // request lengths that this launch takes
+  int K, N, r;
   uint32_t spin;
 };
 
 // Pieces first, first + stride, .. (at most `cap`, from the `skip`-th of them) of
-// TT rows, into `table`, by the whole CTA; their number.  Each thread counts the
+// TT rows, of all requests or (only >= 0) of one adapter's, into `table`, by the
+// whole CTA; their number.  Each thread counts the
 // pieces of a run of requests, a scan locates them, and each thread writes those
 // of its run that are asked for.  `sm` holds NT / 32 + 1 ints.
 template <int NT>
-__device__ __forceinline__ int lora_find_pieces(const LoraArgs& a, int TT, int first, int stride,
-                                                int skip, LoraPiece* table, int cap, int* sm) {
+__device__ __forceinline__ int lora_find_pieces(const LoraRequests& a, int TT, int first,
+                                                int stride, int skip, LoraPiece* table, int cap,
+                                                int* sm, int only = -1) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.nreq + NT - 1) / NT;
   const int q0 = min(a.nreq, tid * per), q1 = min(a.nreq, q0 + per);
   int own = 0;
-  for (int q = q0; q < q1; ++q) own += lora_pieces(a.starts, q, a.m, TT, a.min_len, a.max_len);
+  auto pieces = [&](int q) {
+    return only >= 0 && a.adapter[q] != only
+               ? 0
+               : lora_pieces(a.starts, q, a.m, TT, a.min_len, a.max_len);
+  };
+  for (int q = q0; q < q1; ++q) own += pieces(q);
   int inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -257,7 +274,7 @@ __device__ __forceinline__ int lora_find_pieces(const LoraArgs& a, int TT, int f
   const int64_t p0 = first + (int64_t)skip * stride;
   const int64_t n = total > p0 ? min((int64_t)cap, (total - p0 + stride - 1) / stride) : 0;
   for (int q = q0; q < q1; ++q) {
-    const int c = lora_pieces(a.starts, q, a.m, TT, a.min_len, a.max_len);
+    const int c = pieces(q);
     if (c > 0) {
       int64_t i = at <= p0 ? 0 : (at - p0 + stride - 1) / stride;
       for (; i < n && p0 + i * stride < at + c; ++i) {

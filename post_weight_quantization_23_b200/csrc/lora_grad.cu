@@ -3,7 +3,27 @@
 //   dA_a = sum_t U[t] x_t^T,   dB_a = sum_t dY[t] V[t]^T,
 // t over the rows of adapter a's requests.  Both are sums over tokens of a wide
 // row (x or dY, `S` below) times a narrow fp32 row (U or V, `W` below).
+//
+// Bound by HBM: the wide rows are read once (2 bytes or, from an 8-bit checkpoint,
+// 1 + 4/128 per element) against 2 r flops per element.  Tensor-core kernel: a CTA
+// sums 128 columns of one gradient over the adapter's tokens (or over every SPLIT-th
+// 64-token tile of them; the SPLIT CTAs of a cluster then add up through distributed
+// shared memory in a fixed order), D[128 x RP] fp32 in TMEM, tokens as the MMA's K.
+// Both operands are MN-major: rows of S as TMA brings them, and rows of W.
+//   W is split into two bf16 parts, hi + lo (16 significant bits; bf16 for its range:
+//     gradients are small, f16 would lose them among its subnormals).
+//   S in bf16 is used as it is.  S in f16 is split into two bf16 parts as well (exact but
+//     for f16's smallest subnormals), three products, lo x lo left out.
+//   S in 8-bit codes becomes bf16 exactly (|code| <= 127), and its scales, one per token
+//     and 128-column block, multiply the rows of W: the checkpoint is never restored.
+// Rows behind a request's end in its last tile belong to others (or hold anything):
+// both operands are zeroed there.
+// Warps: 0 TMA, 1 MMA, 2..9 operands (two groups of four, tile by tile in turn) and
+// epilogue.  Every wait is bounded; a CTA that gives up writes NaN.
 #include "lora.cuh"
+#include "tc_ptx.cuh"
+
+#include <algorithm>
 
 namespace gptq {
 
@@ -20,10 +40,8 @@ struct LoraGradArgs {
   int C;
 };
 
-struct LoraGradCommon {
-  const int32_t* starts;
-  const int32_t* adapter;
-  int m, r, na, nreq;
+struct LoraGradCommon : LoraRequests {
+  int r;
   uint32_t spin;
 };
 
@@ -96,14 +114,360 @@ gptq_status grad_general(const LoraGradArgs& a, const LoraGradCommon& c, bool bf
   return GPTQ_OK;
 }
 
+// ---- tensor-core kernel ------------------------------------------------------------
+
+constexpr int GT_C = 128, GT_T = 64;         // columns and tokens of a tile
+constexpr int GT_OPW = 8;                    // operand warps
+constexpr int GT_THREADS = 64 + 32 * GT_OPW;
+constexpr int GT_ATOM = GT_T * 128;          // 64 tokens x 64 16-bit columns, 8 KB
+constexpr int GT_TABLE = 256;                // tiles looked up at a time
+constexpr int GT_LD = GT_C + 1;              // row stride of the staged sums (no bank conflicts)
+
+// Bytes of a stage: S operand hi (and lo), the tile as TMA brought it where it has to
+// be converted (bf16 arrives in place), W hi and lo.
+template <int RP, bool F16>
+struct GtShape {
+  static constexpr int W = (RP > 64 ? 2 : 1) * GT_ATOM;
+  static constexpr int HI = 0, LO = 2 * GT_ATOM;
+  static constexpr int RAW = F16 ? 4 * GT_ATOM : 2 * GT_ATOM;
+  static constexpr int WHI = RAW + (F16 ? 2 : 1) * GT_ATOM, WLO = WHI + W;
+  static constexpr int STAGE = WLO + W;
+  static constexpr int S = F16 ? (RP > 64 ? 2 : 3) : (RP > 64 ? 3 : 5);
+  static constexpr int SUMS = RP * GT_LD * 4;
+  static constexpr size_t SMEM = (size_t)S * STAGE + 256 + GT_TABLE * sizeof(LoraPiece);
+  static_assert(SUMS <= S * STAGE && SMEM <= 232448, "shared memory of a CTA");
+};
+
+// hi + lo in bf16 of four f16 pairs.
+__device__ __forceinline__ void gt_split_f16(uint4 u, uint4& hi, uint4& lo) {
+  const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = LoraType<false>::unpack(in[i]);
+    lora_split<true>(v.x, v.y, h[i], l[i]);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Eight int8 codes as bf16, exactly: 2^23 + 2^7 + code in the low byte of a float.
+__device__ __forceinline__ uint4 gt_codes(uint32_t a, uint32_t b) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = (i < 2 ? a : b) ^ 0x80808080u;  // code + 128
+    const uint32_t s = 2 * (i % 2);
+    const float x = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | s)) - 8388736.f;
+    const float y = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (s + 1))) - 8388736.f;
+    o[i] = LoraType<true>::pack(x, y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int RP, bool F16>
+__global__ void __launch_bounds__(GT_THREADS, 1)
+lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                 LoraGradArgs ga, LoraGradArgs gb, LoraGradCommon c, int blocks_a, int split) {
+  using Sh = GtShape<RP, F16>;
+  using T = typename LoraType<!F16>::T;
+  constexpr int S = Sh::S;
+  extern __shared__ __align__(1024) uint8_t gt_smem[];
+  uint64_t* bars = (uint64_t*)(gt_smem + S * Sh::STAGE);
+  uint64_t* full = bars;            // [S] the tile landed
+  uint64_t* ready = bars + S;       // [S] both operands are written
+  uint64_t* empty = bars + 2 * S;   // [S] the MMAs that read them are done
+  uint64_t* done = bars + 3 * S;
+  uint32_t* tmem_slot = (uint32_t*)(done + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* issued = abort_flag + 1;
+  int* scan = (int*)(tmem_slot + 3);  // GT_THREADS / 32 + 1 ints
+  LoraPiece* table = (LoraPiece*)(gt_smem + S * Sh::STAGE + 256);
+  static_assert((3 * S + 1) * 8 + 12 + 44 <= 256, "fits");
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int part = (int)blockIdx.x % split, blk = (int)blockIdx.x / split;
+  const bool second = blk >= blocks_a;
+  const LoraGradArgs& g = second ? gb : ga;
+  const CUtensorMap* map = second ? &bmap : &amap;
+  const int col0 = (second ? blk - blocks_a : blk) * GT_C, ad = blockIdx.y;
+  const bool codes = g.s_scales != nullptr;
+  constexpr int TM = RP < 32 ? 32 : RP;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&ready[s], 4);
+      tc::mbar_init(&empty[s], 1);
+    }
+    tc::mbar_init(done, 1);
+    *abort_flag = 0;
+    *issued = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tensormap(map);
+  }
+  pdl_wait();
+  pdl_trigger();
+  int np = lora_find_pieces<GT_THREADS>(c, GT_T, part, split, 0, table, GT_TABLE, scan, ad);
+  if (warp == 1) tc::tmem_alloc(tmem_slot, TM);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto stage = [&](int it) { return gt_smem + (size_t)(it % S) * Sh::STAGE; };
+  int base = 0;  // tiles of the tables before
+
+  for (int chunk = 1; np > 0; ++chunk) {
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int i = 0; i < np; ++i) {
+          const int it = base + i, s = it % S;
+          if (it >= S && !tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, c.spin))
+            break;
+          uint8_t* sb = stage(it);
+          const int t0 = table[i].t0;
+          if (codes) {
+            tc::mbar_arrive_expect_tx(&full[s], GT_ATOM);
+            tc::tma_load_2d(sb + Sh::RAW, map, &full[s], col0, t0);
+          } else {
+            uint8_t* dst = sb + (F16 ? Sh::RAW : Sh::HI);
+            tc::mbar_arrive_expect_tx(&full[s], 2 * GT_ATOM);
+            tc::tma_load_2d(dst, map, &full[s], col0, t0);
+            tc::tma_load_2d(dst + GT_ATOM, map, &full[s], col0 + 64, t0);
+          }
+          *issued = it + 1;
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        const uint32_t id = tc::instr_desc(1, GT_C, RP, 1, 1);  // bf16, both MN-major
+        for (int i = 0; i < np; ++i) {
+          const int it = base + i, s = it % S;
+          const uint32_t ph = (uint32_t)(it / S) & 1u;
+          if (!tc::mbar_wait(&full[s], ph, abort_flag, c.spin)) break;
+          if (!tc::mbar_wait(&ready[s], ph, abort_flag, c.spin)) break;
+          tc::tc_fence_after();
+          const uint32_t sb = tc::smem_u32(stage(it));
+          auto mma = [&](int x, int w, int kk, bool first) {
+            tc::mma_f16_ss(tmem, tc::smem_desc_sw128(sb + x + kk * 2048, GT_ATOM, 1024),
+                           tc::smem_desc_sw128(sb + w + kk * 2048, GT_ATOM, 1024), id,
+                           first ? 0u : 1u);
+          };
+#pragma unroll
+          for (int kk = 0; kk < GT_T / 16; ++kk) {
+            mma(Sh::HI, Sh::WLO, kk, it == 0 && kk == 0);
+            if (F16 && !codes) mma(Sh::LO, Sh::WHI, kk, false);
+            mma(Sh::HI, Sh::WHI, kk, false);
+          }
+          tc::mma_commit(&empty[s]);
+        }
+      }
+    } else {
+      // ---- operands: group `grp` of four warps takes every second tile ----
+      const int grp = (warp - 2) / 4, gt = (warp - 2) % 4 * 32 + lane;
+      constexpr int NCH = RP / 8;                 // 8-value chunks of a row of W
+      constexpr int TASKS = GT_T * NCH / 128;     // chunks per thread
+      const int nb = (g.C + 127) / 128;
+      float4 w[TASKS][2];
+      float sc[TASKS];
+      auto fetch = [&](int i) {
+        const LoraPiece p = table[i];
+#pragma unroll
+        for (int k = 0; k < TASKS; ++k) {
+          const int e = gt + 128 * k, t = e / NCH, ch = e % NCH;
+          const bool have = t < p.cnt && 8 * ch < c.r;
+          const float* src = g.W + (int64_t)(p.t0 + t) * c.r + 8 * ch;
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+          w[k][0] = have ? __ldg(reinterpret_cast<const float4*>(src)) : z;
+          w[k][1] = have ? __ldg(reinterpret_cast<const float4*>(src) + 1) : z;
+          sc[k] = codes && have ? __ldg(g.s_scales + (int64_t)(p.t0 + t) * nb + col0 / 128) : 1.f;
+        }
+      };
+      int i = ((base & 1) == grp) ? 0 : 1;
+      if (i < np) fetch(i);
+      for (; i < np; i += 2) {
+        const int it = base + i, s = it % S;
+        const int cnt = table[i].cnt;
+        if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, c.spin)) break;
+        uint8_t* sb = stage(it);
+#pragma unroll
+        for (int k = 0; k < TASKS; ++k) {
+          const int e = gt + 128 * k, t = e / NCH, ch = e % NCH;
+          const float f = sc[k];
+          uint4 hi, lo;
+          lora_split<true>(w[k][0].x * f, w[k][0].y * f, hi.x, lo.x);
+          lora_split<true>(w[k][0].z * f, w[k][0].w * f, hi.y, lo.y);
+          lora_split<true>(w[k][1].x * f, w[k][1].y * f, hi.z, lo.z);
+          lora_split<true>(w[k][1].z * f, w[k][1].w * f, hi.w, lo.w);
+          const int o = (ch / 8) * GT_ATOM + t * 128 + (((ch % 8) ^ (t & 7)) << 4);
+          *reinterpret_cast<uint4*>(sb + Sh::WHI + o) = hi;
+          *reinterpret_cast<uint4*>(sb + Sh::WLO + o) = lo;
+        }
+        if (i + 2 < np) fetch(i + 2);
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        if (codes) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // 16 codes each
+            const int e = gt + 128 * k, t = e / 8, j = e % 8;
+            const uint4 q = *reinterpret_cast<const uint4*>(sb + Sh::RAW + t * 128 + 16 * j);
+            const bool have = t < cnt;
+            uint8_t* row = sb + Sh::HI + (j / 4) * GT_ATOM + t * 128;
+            const int ch = 2 * (j % 4);
+            *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = have ? gt_codes(q.x, q.y) : z;
+            *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) =
+                have ? gt_codes(q.z, q.w) : z;
+          }
+        } else if (F16) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {  // 8 values each; the swizzle stays as TMA laid it
+            const int e = gt + 128 * k;
+            const bool have = (e % 512) / 8 < cnt;
+            uint4 hi = z, lo = z;
+            if (have) gt_split_f16(*reinterpret_cast<const uint4*>(sb + Sh::RAW + 16 * e), hi, lo);
+            *reinterpret_cast<uint4*>(sb + Sh::HI + 16 * e) = hi;
+            *reinterpret_cast<uint4*>(sb + Sh::LO + 16 * e) = lo;
+          }
+        } else if (cnt < GT_T) {
+          for (int e = gt; e < 2 * GT_ATOM / 16; e += 128)
+            if ((e % 512) / 8 >= cnt) *reinterpret_cast<uint4*>(sb + Sh::HI + 16 * e) = z;
+        }
+        tc::fence_proxy_async_smem();  // the MMA reads what this thread wrote
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ready[s]);
+      }
+    }
+    __syncthreads();
+    base += np;
+    if (np < GT_TABLE || *abort_flag) break;
+    np = lora_find_pieces<GT_THREADS>(c, GT_T, part, split, chunk * GT_TABLE, table, GT_TABLE, scan,
+                                      ad);
+  }
+  // all MMAs done (their stages are free for the sums), all copies landed
+  if (warp == 1 && lane == 0) tc::mma_commit(done);
+  const bool finished = tc::mbar_wait_warp(done, 0, abort_flag, tc::kSpinLimit);
+  if (*abort_flag && threadIdx.x == 0)
+    for (int p = max(0, *issued - S); p < *issued; ++p)
+      for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
+        if (tc::mbar_try_wait(&full[p % S], (uint32_t)(p / S) & 1u)) break;
+  __syncthreads();
+  tc::tc_fence_after();
+  const bool ok = finished && !*abort_flag;
+  float* sums = (float*)gt_smem;  // [RP][GT_LD]
+  if (warp >= 2) {
+    const int quarter = warp & 3, hf = (warp - 2) / 4, col = quarter * 32 + lane;
+    constexpr int HC = RP / 2, CW = HC < 32 ? HC : 32;
+#pragma unroll
+    for (int q = 0; q < HC; q += CW) {
+      float v[CW];
+      const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(hf * HC + q);
+      if (CW == 8) tc::tmem_ld_32x32b_x8(ta, v);
+      else if (CW == 16) tc::tmem_ld_32x32b_x16(ta, v);
+      else tc::tmem_ld_32x32b_x32(ta, v);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < CW; ++e)
+        sums[(hf * HC + q + e) * GT_LD + col] =
+            !ok ? __int_as_float(0x7fc00000) : base > 0 ? v[e] : 0.f;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(tmem, TM);
+  if (split > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  // this CTA's share of the columns, summed over the cluster
+  const int per = GT_C / split, c0 = part * per;
+  T* out = (T*)g.out + (int64_t)ad * c.r * g.C;
+  for (int e = threadIdx.x; e < per * c.r; e += GT_THREADS) {
+    // neighbouring threads along the axis that is contiguous in the output
+    const int cc = g.col_stride == 1 ? c0 + e % per : c0 + e / c.r;
+    const int p = g.col_stride == 1 ? e / per : e % c.r;
+    float v = 0.f;
+    if (split == 1) {
+      v = sums[p * GT_LD + cc];
+    } else {
+      const uint32_t at = tc::smem_u32(sums + p * GT_LD + cc);
+      for (int q = 0; q < split; ++q) v += cluster_ld_f32(cluster_map(at, (uint32_t)q));
+    }
+    if (col0 + cc < g.C)
+      out[(int64_t)(col0 + cc) * g.col_stride + (int64_t)p * g.rank_stride] = LoraType<!F16>::cvt(v);
+  }
+  if (split > 1) {  // no CTA leaves while another reads its sums
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
+bool gt_supported(const LoraGradArgs& g) {
+  const int64_t ldb = g.lds * (g.s_scales != nullptr ? 1 : 2);
+  return (uintptr_t)g.S % 16 == 0 && ldb % 16 == 0 && (uintptr_t)g.W % 16 == 0 &&
+         tensormap_encoder() != nullptr;
+}
+
+bool gt_map(CUtensorMap* map, const LoraGradArgs& g, int m, bool bf16) {
+  const bool codes = g.s_scales != nullptr;
+  cuuint64_t gdim[2] = {(cuuint64_t)g.C, (cuuint64_t)m};
+  cuuint64_t gstride[1] = {(cuuint64_t)g.lds * (codes ? 1 : 2)};
+  cuuint32_t box[2] = {codes ? 128u : 64u, GT_T};
+  cuuint32_t es[2] = {1, 1};
+  return tensormap_encoder()(
+             map,
+             codes  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+             : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             2, const_cast<void*>(g.S), gdim, gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// dA and dB in one launch (`with_a`, `with_b`: those that TMA can read).
+template <int RP, bool F16>
+gptq_status launch_grad(const LoraGradArgs& ga, const LoraGradArgs& gb, const LoraGradCommon& c,
+                        bool with_a, bool with_b, cudaStream_t s) {
+  using Sh = GtShape<RP, F16>;
+  CUtensorMap am, bm;
+  bool ok = true;
+  if (with_a) ok = ok && gt_map(&am, ga, c.m, !F16);
+  if (with_b) ok = ok && gt_map(&bm, gb, c.m, !F16);
+  if (!with_a) am = bm;
+  if (!with_b) bm = am;
+  if (!ok || smem_optin((const void*)lora_grad_kernel<RP, F16>, Sh::SMEM) != cudaSuccess)
+    return GPTQ_ERR_CUDA;
+  const int ba = with_a ? (int)cdiv(ga.C, GT_C) : 0, bb = with_b ? (int)cdiv(gb.C, GT_C) : 0;
+  // tokens split over a cluster while the CTAs still fit the device at once and keep a few
+  // tiles each
+  const int64_t ctas = (int64_t)(ba + bb) * c.na, tiles = cdiv(c.m, GT_T) / c.na;
+  int split = 1;
+  while (split < 8 && ctas * split * 2 <= sm_count() && tiles / (split * 2) >= 4) split *= 2;
+  launch_cluster_pdl(lora_grad_kernel<RP, F16>, dim3((unsigned)((ba + bb) * split), (unsigned)c.na),
+                     dim3(GT_THREADS), Sh::SMEM, split, s, am, bm, ga, gb, c, ba, split);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
+template <bool F16>
+gptq_status grad_ranks(const LoraGradArgs& ga, const LoraGradArgs& gb, const LoraGradCommon& c,
+                       bool with_a, bool with_b, cudaStream_t s) {
+  if (c.r <= 16) return launch_grad<16, F16>(ga, gb, c, with_a, with_b, s);
+  if (c.r <= 32) return launch_grad<32, F16>(ga, gb, c, with_a, with_b, s);
+  if (c.r <= 64) return launch_grad<64, F16>(ga, gb, c, with_a, with_b, s);
+  return launch_grad<128, F16>(ga, gb, c, with_a, with_b, s);
+}
+
 }  // namespace
 
 // dA (na, r, k) and dB (na, n, r) from U, V (m, r).
 gptq_status lora_grads_impl(const LoraGradArgs& ga, const LoraGradArgs& gb,
                             const LoraGradCommon& c, bool bf16, cudaStream_t s) {
-  gptq_status st = grad_general(ga, c, bf16, s);
-  if (st != GPTQ_OK) return st;
-  return grad_general(gb, c, bf16, s);
+  const bool with_a = c.m > 0 && c.nreq > 0 && gt_supported(ga);
+  const bool with_b = c.m > 0 && c.nreq > 0 && gt_supported(gb);
+  gptq_status st = GPTQ_OK;
+  if (!with_a) st = grad_general(ga, c, bf16, s);
+  if (st == GPTQ_OK && !with_b) st = grad_general(gb, c, bf16, s);
+  if (st != GPTQ_OK || (!with_a && !with_b)) return st;
+  return bf16 ? grad_ranks<false>(ga, gb, c, with_a, with_b, s)
+              : grad_ranks<true>(ga, gb, c, with_a, with_b, s);
 }
 
 gptq_status lora_backward_impl(LoraArgs low, const void* X, int64_t ldx, const float* x_scales,
@@ -115,6 +479,7 @@ gptq_status lora_backward_impl(LoraArgs low, const void* X, int64_t ldx, const f
   const int k = low.N, n = low.K, r = low.r;
   LoraGradCommon c;
   c.starts = low.starts, c.adapter = low.adapter;
+  c.min_len = 1, c.max_len = low.m;
   c.m = low.m, c.r = r, c.na = low.na, c.nreq = low.nreq, c.spin = low.spin;
   LoraGradArgs ga, gb;
   ga.S = X, ga.lds = ldx, ga.s_scales = x_scales, ga.W = low.V, ga.out = dA;
