@@ -356,10 +356,10 @@ GPTQ_API gptq_status gptq_rotate(const void* in, gptq_dtype dt, int64_t rows, in
  *           overlap dY.
  *   m <= 131070 tokens.  The library allocates nothing.
  * Kernel choice:
- *   4-bit, g_idx NULL, group_size a multiple of 8 (or one group per row), dY
+ *   4-bit, g_idx NULL, group_size a multiple of 32 (or one group per row), dY
  *     16-byte aligned with lddy % 8 == 0 and qweight 16-byte aligned: the
  *     tensor-core kernel (each weight formed from the fp32 scale and rounded
- *     once to dt; fp32 accumulation);
+ *     once to dt; |zeros| <= 127; fp32 accumulation);
  *   every other case: the general kernel (fp32 weights and products).
  * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_UNSUPPORTED (bits, f32 dY),
  * GPTQ_ERR_CUDA.  A bounded wait of the tensor-core kernel that gave up writes

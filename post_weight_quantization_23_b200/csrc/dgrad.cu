@@ -3,7 +3,31 @@
 //   dX[t, c] = sum_j dY[t, j] scale[j, g(c)] (code[j, c] - zero[j, g(c)]).
 // The reduction runs over the rows of W, the output over its columns: the other
 // way round than gptq_gemm over the same packed words.
+//
+// Bound by the tensor cores from a few hundred tokens on (2 m n k flops against
+// n k / 2 + 2 m (n + k) bytes).  Tensor-core kernel: one CTA per MT * 128 columns x N
+// tokens, the rows of W in stages of 64:
+//   warp 0       TMA: the packed words of the 64 rows (MT * 64 bytes each, swizzled
+//                so that 8 rows read without bank conflicts) and the N x 64 box of dY;
+//   warps 2..17  two groups of eight, stage by stage in turn: a thread turns 32 codes
+//                of one row into weights, two at a time.  A byte permute and a mask
+//                put codes c_2i, c_2i+1 into the mantissas of a pair M + c (M = 1024
+//                for f16, 128 for bf16), M + zero is subtracted: c - zero, exactly.
+//                The fp32 scale is split into two 16-bit parts, and
+//                w = fl(d * s_hi + fl(d * s_lo)): the product with the fp32 scale
+//                rounded once (f16 bf16: 2^-11, 2^-8), where a scale rounded first
+//                would add its own error.  The codes of a word are neighbours along
+//                the output axis, so the weights are written as an MN-major operand,
+//                16 bytes per word;
+//   warp 1       kind::f16 MMAs D[128 x N] += W^T dY^T per 128 columns, fp32 in TMEM.
+// The 16 warps are the epilogue too (TMEM lane = column, TMEM column = token).
+// MT = 2 halves the stages' dY traffic and the launch picks N (launch_shape).
+// Every wait is bounded; a CTA that gives up drains its copies and MMAs, frees TMEM and
+// writes NaN over its outputs.
 #include "common.cuh"
+#include "tc_ptx.cuh"
+
+#include <algorithm>
 
 namespace gptq {
 
@@ -86,6 +110,282 @@ dgrad_general_kernel(const T* __restrict__ dY, int64_t lddy, int m, int n,
     }
 }
 
+// ---- tensor-core kernel ------------------------------------------------------------
+
+constexpr int DT_K = 64;                    // rows of W per stage
+constexpr int DT_GROUP = 8;                 // warps of a dequantizing group
+constexpr int DT_THREADS = 64 + 2 * 32 * DT_GROUP;
+constexpr int DT_NMAX = 256;
+
+template <int MT>
+struct DtShape {
+  static constexpr int A = MT * 128 * DT_K * 2;   // weights
+  static constexpr int B = DT_NMAX * DT_K * 2;    // dY
+  static constexpr int P = MT * 128 * DT_K / 2;   // packed words
+  static constexpr int STAGE = A + B + P;
+  static constexpr int S = MT == 2 ? 3 : 4;
+  static constexpr size_t SMEM = (size_t)S * STAGE + 256;
+  static_assert(SMEM <= 232448 && STAGE % 1024 == 0, "shared memory of a CTA");
+};
+
+struct DtArgs {
+  const float* scales;
+  const int32_t* zeros;
+  void* dX;
+  int64_t lddx;
+  int n, m, k, G, ngroups;
+  int N;          // tokens of a tile
+  uint32_t spin;  // polls before a pipeline wait gives up
+};
+
+template <bool BF16> struct DtType;
+template <> struct DtType<false> {
+  using T = __half;
+  using T2 = __half2;
+  static constexpr uint32_t MAGIC = 0x64006400u;  // 1024 in both halves: ulp 1 on [1024, 2048)
+  static constexpr float BASE = 1024.f;
+  __device__ static T2 pair(float v) { return __float2half2_rn(v); }
+  __device__ static float back(T2 v) { return __low2float(v); }
+};
+template <> struct DtType<true> {
+  using T = __nv_bfloat16;
+  using T2 = __nv_bfloat162;
+  static constexpr uint32_t MAGIC = 0x43004300u;  // 128 in both halves: ulp 1 on [128, 256)
+  static constexpr float BASE = 128.f;
+  __device__ static T2 pair(float v) { return __float2bfloat162_rn(v); }
+  __device__ static float back(T2 v) { return __low2float(v); }
+};
+
+template <bool BF16, int MT>
+__global__ void __launch_bounds__(DT_THREADS, 1)
+dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap pmap,
+                DtArgs a) {
+  using Ty = DtType<BF16>;
+  using T2 = typename Ty::T2;
+  using Sh = DtShape<MT>;
+  constexpr int S = Sh::S;
+  extern __shared__ __align__(1024) uint8_t dt_smem[];
+  uint64_t* bars = (uint64_t*)(dt_smem + S * Sh::STAGE);
+  uint64_t* full = bars;            // [S] packed words and dY landed
+  uint64_t* ready = bars + S;       // [S] the weights are written
+  uint64_t* empty = bars + 2 * S;   // [S] the stage's MMAs are done
+  uint64_t* done = bars + 3 * S;
+  uint32_t* tmem_slot = (uint32_t*)(done + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* issued = abort_flag + 1;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int c0 = blockIdx.x * (MT * 128), t0 = blockIdx.y * a.N;
+  const int ns = (a.n + DT_K - 1) / DT_K;
+  auto stage = [&](int it) { return dt_smem + (size_t)(it % S) * Sh::STAGE; };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&ready[s], DT_GROUP);
+      tc::mbar_init(&empty[s], 1);
+    }
+    tc::mbar_init(done, 1);
+    *abort_flag = 0;
+    *issued = 0;
+    tc::fence_barrier_init();
+    tc::prefetch_tensormap(&ymap);
+    tc::prefetch_tensormap(&pmap);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 1) tc::tmem_alloc(tmem_slot, MT * 256);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t bytes = Sh::P + (uint32_t)a.N * DT_K * 2;
+      for (int it = 0; it < ns; ++it) {
+        const int s = it % S;
+        if (it >= S && !tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, a.spin))
+          break;
+        uint8_t* sb = stage(it);
+        tc::mbar_arrive_expect_tx(&full[s], bytes);
+        tc::tma_load_2d(sb + Sh::A + Sh::B, &pmap, &full[s], c0 / 8, it * DT_K);
+        tc::tma_load_2d(sb + Sh::A, &ymap, &full[s], it * DT_K, t0);
+        *issued = it + 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = tc::instr_desc(BF16 ? 1 : 0, 128, a.N, 1, 0);  // W MN-major, dY K-major
+      for (int it = 0; it < ns; ++it) {
+        const int s = it % S;
+        const uint32_t ph = (uint32_t)(it / S) & 1u;
+        if (!tc::mbar_wait(&full[s], ph, abort_flag, a.spin)) break;
+        if (!tc::mbar_wait(&ready[s], ph, abort_flag, a.spin)) break;
+        tc::tc_fence_after();
+        const uint32_t sa = tc::smem_u32(stage(it)), sy = sa + Sh::A;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int kk = 0; kk < DT_K / 16; ++kk)
+            tc::mma_f16_ss(tmem + 256 * mt,
+                           tc::smem_desc_sw128(sa + mt * 16384 + kk * 2048, 8192, 1024),
+                           tc::smem_desc_sw128(sy + kk * 32, 16, 1024), id,
+                           (it > 0 || kk > 0) ? 1u : 0u);
+        tc::mma_commit(&empty[s]);
+      }
+      tc::mma_commit(done);  // fires once every MMA issued above has finished
+    }
+  } else {
+    const int grp = (warp - 2) / DT_GROUP, gw = (warp - 2) % DT_GROUP;
+    // MT == 2: quad (32 columns) gw of rows lane and lane + 32; MT == 1: quad gw % 4 of
+    // row lane + 32 (gw / 4).  Neighbouring lanes are neighbouring rows.
+    constexpr int R = MT;
+    const int quad = MT == 2 ? gw : gw % 4, j0 = lane + (MT == 2 ? 0 : 32 * (gw / 4));
+    const int col = c0 + 32 * quad;
+    const int g = min(col, a.k - 1) / a.G;
+    float sc[R], ze[R];
+    auto fetch = [&](int it) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int j = it * DT_K + j0 + 32 * r;
+        const bool ok = it < ns && j < a.n;
+        sc[r] = ok ? __ldg(a.scales + (int64_t)j * a.ngroups + g) : 0.f;
+        ze[r] = ok ? (float)__ldg(a.zeros + (int64_t)j * a.ngroups + g) : 0.f;
+      }
+    };
+    fetch(grp);
+    for (int it = grp; it < ns; it += 2) {
+      const int s = it % S;
+      T2 hi[R], lo[R], zz[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        hi[r] = Ty::pair(sc[r]);
+        lo[r] = Ty::pair(sc[r] - Ty::back(hi[r]));
+        zz[r] = Ty::pair(Ty::BASE + ze[r]);  // exact for |zero| <= 127
+      }
+      fetch(it + 2);
+      if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin)) break;
+      uint8_t* sb = stage(it);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int j = j0 + 32 * r;
+        const int pos = MT == 2 ? j * 128 + ((quad ^ (j & 7)) << 4)          // 128-byte swizzle
+                                : j * 64 + ((quad ^ ((j >> 1) & 3)) << 4);   // 64-byte swizzle
+        const uint4 pw = *reinterpret_cast<const uint4*>(sb + Sh::A + Sh::B + pos);
+        const uint32_t words[4] = {pw.x, pw.y, pw.z, pw.w};
+        uint8_t* row = sb + (quad / 2) * 8192 + j * 128;  // 64-column atoms
+#pragma unroll
+        for (int wi = 0; wi < 4; ++wi) {
+          const uint32_t w = words[wi], w4 = w >> 4;
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // byte i of w (c_2i low) into half 0, byte i of w >> 4 (c_2i+1 low) into half 1
+            const uint32_t v =
+                __byte_perm(w, w4, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | (i << 12)));
+            const uint32_t h = (v & 0x000F000Fu) | Ty::MAGIC;               // M + c, exact
+            const T2 d = __hsub2(*reinterpret_cast<const T2*>(&h), zz[r]);  // c - zero, exact
+            const T2 x = __hfma2(d, hi[r], __hmul2(d, lo[r]));
+            o[i] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          *reinterpret_cast<uint4*>(row + ((((quad % 2) * 4 + wi) ^ (j & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      tc::fence_proxy_async_smem();  // the MMA reads what this thread wrote
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&ready[s]);
+    }
+    // epilogue: this warp's lane quarter of one 128-column tile, its share of the tokens
+    const bool ok = tc::mbar_wait_warp(done, 0, abort_flag, a.spin) && !*abort_flag;
+    tc::tc_fence_after();
+    const int quarter = warp & 3, set = (warp - 2) / 4;  // 4 sets of 4 warps
+    const int mt = MT == 2 ? set / 2 : 0;
+    const int nset = 4 / MT, which = set % nset;
+    const int c = c0 + mt * 128 + quarter * 32 + lane;
+    typename Ty::T* out = reinterpret_cast<typename Ty::T*>(a.dX) + c;
+    for (int q = which * 32; q < a.N; q += nset * 32) {
+      float v[32];
+      tc::tmem_ld_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(256 * mt + q), v);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int t = 0; t < 32; ++t)
+        if (c < a.k && q + t < a.N && t0 + q + t < a.m)
+          out[(int64_t)(t0 + q + t) * a.lddx] =
+              dg_out<typename Ty::T>(ok ? v[t] : __int_as_float(0x7fc00000));
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) {  // the copies and MMAs in flight end before shared memory and TMEM go
+    if (threadIdx.x == 0)
+      for (int p = max(0, *issued - S); p < *issued; ++p)
+        for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
+          if (tc::mbar_try_wait(&full[p % S], (uint32_t)(p / S) & 1u)) break;
+    if (threadIdx.x == 32)
+      for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
+        if (tc::mbar_try_wait(done, 0)) break;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  if (warp == 1) tc::tmem_dealloc(tmem, MT * 256);
+}
+
+bool dgrad_tc_supported(const void* dY, int64_t lddy, const int32_t* qw, int bits, int64_t k,
+                        int64_t n, int G, bool has_gidx) {
+  return bits == 4 && !has_gidx && n > 0 && (G >= k || G % 32 == 0) && (uintptr_t)dY % 16 == 0 &&
+         lddy % 8 == 0 && (uintptr_t)qw % 16 == 0 && tensormap_encoder() != nullptr;
+}
+
+// Columns (MT * 128) and tokens (N, a multiple of 16) of a tile: the pair whose waves
+// over the SMs cost least, a stage of a wave counted as its MMAs (2 MT N cycles) or its
+// dequantization, whichever is longer.
+void launch_shape(int64_t m, int64_t k, int& MT, int& N) {
+  const int sms = sm_count();
+  double best = 0;
+  for (int mt = 1; mt <= 2; ++mt)
+    for (int nn = 16; nn <= DT_NMAX; nn += 16) {
+      const int64_t tiles = cdiv(k, mt * 128) * cdiv(m, nn);
+      const double cost = (double)cdiv(tiles, sms) * std::max(2.0 * mt * nn, 200.0 * mt + 200.0);
+      if (best == 0 || cost < best * 0.999) best = cost, MT = mt, N = nn;
+    }
+}
+
+template <bool BF16, int MT>
+gptq_status launch_dgrad(const void* dY, int64_t lddy, const int32_t* qw, DtArgs a, cudaStream_t s) {
+  using Sh = DtShape<MT>;
+  EncodeTiledFn enc = tensormap_encoder();
+  CUtensorMap ymap, pmap;
+  cuuint32_t es[2] = {1, 1};
+  {
+    cuuint64_t gdim[2] = {(cuuint64_t)a.n, (cuuint64_t)a.m};
+    cuuint64_t gstride[1] = {(cuuint64_t)lddy * 2};
+    cuuint32_t box[2] = {DT_K, (cuuint32_t)a.N};
+    if (enc(&ymap, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(dY), gdim, gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return GPTQ_ERR_CUDA;
+  }
+  {
+    cuuint64_t gdim[2] = {(cuuint64_t)(a.k / 8), (cuuint64_t)a.n};
+    cuuint64_t gstride[1] = {(cuuint64_t)(a.k / 8) * 4};
+    cuuint32_t box[2] = {MT * 16, DT_K};
+    if (enc(&pmap, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<int32_t*>(qw), gdim, gstride, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            MT == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return GPTQ_ERR_CUDA;
+  }
+  if (smem_optin((const void*)dgrad_tc_kernel<BF16, MT>, Sh::SMEM) != cudaSuccess)
+    return GPTQ_ERR_CUDA;
+  launch_pdl(dgrad_tc_kernel<BF16, MT>,
+             dim3((unsigned)cdiv(a.k, MT * 128), (unsigned)cdiv(a.m, a.N)), dim3(DT_THREADS),
+             Sh::SMEM, s, ymap, pmap, a);
+  GPTQ_CHECK_LAUNCH();
+  return GPTQ_OK;
+}
+
 }  // namespace
 
 gptq_status dgrad_impl(const void* dY, gptq_dtype dt, int64_t m, int64_t n, int64_t lddy,
@@ -93,6 +393,19 @@ gptq_status dgrad_impl(const void* dY, gptq_dtype dt, int64_t m, int64_t n, int6
                        const int32_t* g_idx, int64_t k, int bits, int group_size, int64_t ngroups,
                        void* dX, int64_t lddx, cudaStream_t s) {
   const int G = group_size == -1 ? (int)k : group_size;
+  if (dgrad_tc_supported(dY, lddy, qw, bits, k, n, G, g_idx != nullptr)) {
+    DtArgs a;
+    a.scales = scales, a.zeros = zeros, a.dX = dX, a.lddx = lddx;
+    a.n = (int)n, a.m = (int)m, a.k = (int)k, a.G = G, a.ngroups = (int)ngroups;
+    a.spin = wait_limit();
+    int MT = 1;
+    launch_shape(m, k, MT, a.N);
+    if (dt == GPTQ_BF16)
+      return MT == 2 ? launch_dgrad<true, 2>(dY, lddy, qw, a, s)
+                     : launch_dgrad<true, 1>(dY, lddy, qw, a, s);
+    return MT == 2 ? launch_dgrad<false, 2>(dY, lddy, qw, a, s)
+                   : launch_dgrad<false, 1>(dY, lddy, qw, a, s);
+  }
   const dim3 grid((unsigned)cdiv(k, DG_C), (unsigned)cdiv(m, DG_T));
   if (dt == GPTQ_F16)
     launch_pdl(dgrad_general_kernel<__half>, grid, dim3(256), 0, s, (const __half*)dY, lddy, (int)m,
