@@ -9,8 +9,9 @@
 // tokens, the rows of W in stages of 64:
 //   warp 0       TMA: the packed words of the 64 rows (MT * 64 bytes each, swizzled
 //                so that 8 rows read without bank conflicts) and the N x 64 box of dY;
-//   warps 2..17  two groups of eight, stage by stage in turn: a thread turns 32 codes
-//                of one row into weights, two at a time.  A byte permute and a mask
+//   warps 2..    groups of four, one per stage of the ring (a slot belongs to one group,
+//                which sees every phase of its barrier): a thread turns runs of 32 codes
+//                of a row into weights, two at a time.  A byte permute and a mask
 //                put codes c_2i, c_2i+1 into the mantissas of a pair M + c (M = 1024
 //                for f16, 128 for bf16), M + zero is subtracted: c - zero, exactly.
 //                The fp32 scale is split into two 16-bit parts, and
@@ -20,7 +21,7 @@
 //                the output axis, so the weights are written as an MN-major operand,
 //                16 bytes per word;
 //   warp 1       kind::f16 MMAs D[128 x N] += W^T dY^T per 128 columns, fp32 in TMEM.
-// The 16 warps are the epilogue too (TMEM lane = column, TMEM column = token).
+// The same warps are the epilogue (TMEM lane = column, TMEM column = token).
 // MT = 2 halves the stages' dY traffic and the launch picks N (launch_shape).
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs, frees TMEM and
 // writes NaN over its outputs.
@@ -113,8 +114,7 @@ dgrad_general_kernel(const T* __restrict__ dY, int64_t lddy, int m, int n,
 // ---- tensor-core kernel ------------------------------------------------------------
 
 constexpr int DT_K = 64;                    // rows of W per stage
-constexpr int DT_GROUP = 8;                 // warps of a dequantizing group
-constexpr int DT_THREADS = 64 + 2 * 32 * DT_GROUP;
+constexpr int DT_GROUP = 4;                 // warps of a dequantizing group
 constexpr int DT_NMAX = 256;
 
 template <int MT>
@@ -123,7 +123,8 @@ struct DtShape {
   static constexpr int B = DT_NMAX * DT_K * 2;    // dY
   static constexpr int P = MT * 128 * DT_K / 2;   // packed words
   static constexpr int STAGE = A + B + P;
-  static constexpr int S = MT == 2 ? 3 : 4;
+  static constexpr int S = MT == 2 ? 3 : 4;     // stages, and dequantizing groups
+  static constexpr int THREADS = 64 + 32 * DT_GROUP * S;
   static constexpr size_t SMEM = (size_t)S * STAGE + 256;
   static_assert(SMEM <= 232448 && STAGE % 1024 == 0, "shared memory of a CTA");
 };
@@ -157,7 +158,7 @@ template <> struct DtType<true> {
 };
 
 template <bool BF16, int MT>
-__global__ void __launch_bounds__(DT_THREADS, 1)
+__global__ void __launch_bounds__(DtShape<MT>::THREADS, 1)
 dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap pmap,
                 DtArgs a) {
   using Ty = DtType<BF16>;
@@ -237,24 +238,25 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
     }
   } else {
     const int grp = (warp - 2) / DT_GROUP, gw = (warp - 2) % DT_GROUP;
-    // MT == 2: quad (32 columns) gw of rows lane and lane + 32; MT == 1: quad gw % 4 of
-    // row lane + 32 (gw / 4).  Neighbouring lanes are neighbouring rows.
-    constexpr int R = MT;
-    const int quad = MT == 2 ? gw : gw % 4, j0 = lane + (MT == 2 ? 0 : 32 * (gw / 4));
-    const int col = c0 + 32 * quad;
-    const int g = min(col, a.k - 1) / a.G;
+    // quads (32 columns) MT gw .. of rows lane and lane + 32; neighbouring lanes are
+    // neighbouring rows
+    constexpr int R = 2 * MT;
+    int g[MT];
+#pragma unroll
+    for (int q = 0; q < MT; ++q) g[q] = min(c0 + 32 * (MT * gw + q), a.k - 1) / a.G;
     float sc[R], ze[R];
     auto fetch = [&](int it) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int j = it * DT_K + j0 + 32 * r;
+        const int j = it * DT_K + lane + 32 * (r & 1);
         const bool ok = it < ns && j < a.n;
-        sc[r] = ok ? __ldg(a.scales + (int64_t)j * a.ngroups + g) : 0.f;
-        ze[r] = ok ? (float)__ldg(a.zeros + (int64_t)j * a.ngroups + g) : 0.f;
+        const int64_t at = (int64_t)j * a.ngroups + g[r / 2];
+        sc[r] = ok ? __ldg(a.scales + at) : 0.f;
+        ze[r] = ok ? (float)__ldg(a.zeros + at) : 0.f;
       }
     };
     fetch(grp);
-    for (int it = grp; it < ns; it += 2) {
+    for (int it = grp; it < ns; it += S) {
       const int s = it % S;
       T2 hi[R], lo[R], zz[R];
 #pragma unroll
@@ -263,12 +265,12 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
         lo[r] = Ty::pair(sc[r] - Ty::back(hi[r]));
         zz[r] = Ty::pair(Ty::BASE + ze[r]);  // exact for |zero| <= 127
       }
-      fetch(it + 2);
+      fetch(it + S);
       if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin)) break;
       uint8_t* sb = stage(it);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int j = j0 + 32 * r;
+        const int j = lane + 32 * (r & 1), quad = MT * gw + r / 2;
         const int pos = MT == 2 ? j * 128 + ((quad ^ (j & 7)) << 4)          // 128-byte swizzle
                                 : j * 64 + ((quad ^ ((j >> 1) & 3)) << 4);   // 64-byte swizzle
         const uint4 pw = *reinterpret_cast<const uint4*>(sb + Sh::A + Sh::B + pos);
@@ -296,15 +298,14 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&ready[s]);
     }
-    // epilogue: this warp's lane quarter of one 128-column tile, its share of the tokens
+    // epilogue: this warp's lane quarter of the 128-column tiles, its share of the tokens
     const bool ok = tc::mbar_wait_warp(done, 0, abort_flag, a.spin) && !*abort_flag;
     tc::tc_fence_after();
-    const int quarter = warp & 3, set = (warp - 2) / 4;  // 4 sets of 4 warps
-    const int mt = MT == 2 ? set / 2 : 0;
-    const int nset = 4 / MT, which = set % nset;
-    const int c = c0 + mt * 128 + quarter * 32 + lane;
-    typename Ty::T* out = reinterpret_cast<typename Ty::T*>(a.dX) + c;
-    for (int q = which * 32; q < a.N; q += nset * 32) {
+    const int quarter = warp & 3, nch = (a.N + 31) / 32;  // 32-token chunks of a tile
+    for (int x = grp; x < MT * nch; x += S) {
+      const int mt = x / nch, q = x % nch * 32;
+      const int c = c0 + mt * 128 + quarter * 32 + lane;
+      typename Ty::T* out = reinterpret_cast<typename Ty::T*>(a.dX) + c;
       float v[32];
       tc::tmem_ld_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(256 * mt + q), v);
       tc::tmem_ld_wait();
@@ -380,7 +381,7 @@ gptq_status launch_dgrad(const void* dY, int64_t lddy, const int32_t* qw, DtArgs
   if (smem_optin((const void*)dgrad_tc_kernel<BF16, MT>, Sh::SMEM) != cudaSuccess)
     return GPTQ_ERR_CUDA;
   launch_pdl(dgrad_tc_kernel<BF16, MT>,
-             dim3((unsigned)cdiv(a.k, MT * 128), (unsigned)cdiv(a.m, a.N)), dim3(DT_THREADS),
+             dim3((unsigned)cdiv(a.k, MT * 128), (unsigned)cdiv(a.m, a.N)), dim3(Sh::THREADS),
              Sh::SMEM, s, ymap, pmap, a);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;

@@ -18,8 +18,10 @@
 //     and 128-column block, multiply the rows of W: the checkpoint is never restored.
 // Rows behind a request's end in its last tile belong to others (or hold anything):
 // both operands are zeroed there.
-// Warps: 0 TMA, 1 MMA, 2..9 operands (two groups of four, tile by tile in turn) and
-// epilogue.  Every wait is bounded; a CTA that gives up writes NaN.
+// Warps: 0 TMA, 1 MMA, then the operand warps (groups of four, tile by tile in turn),
+// which are the epilogue too.  The number of stages is a multiple of the groups, so a
+// slot belongs to one group, which sees every phase of its barrier (a wait that skips
+// phases cannot tell the one before from the one it wants).  Every wait is bounded; a CTA that gives up writes NaN.
 #include "lora.cuh"
 #include "tc_ptx.cuh"
 
@@ -117,10 +119,8 @@ gptq_status grad_general(const LoraGradArgs& a, const LoraGradCommon& c, bool bf
 // ---- tensor-core kernel ------------------------------------------------------------
 
 constexpr int GT_C = 128, GT_T = 64;         // columns and tokens of a tile
-constexpr int GT_OPW = 8;                    // operand warps
-constexpr int GT_THREADS = 64 + 32 * GT_OPW;
 constexpr int GT_ATOM = GT_T * 128;          // 64 tokens x 64 16-bit columns, 8 KB
-constexpr int GT_TABLE = 256;                // tiles looked up at a time
+constexpr int GT_TABLE = 128;                // tiles looked up at a time
 constexpr int GT_LD = GT_C + 1;              // row stride of the staged sums (no bank conflicts)
 
 // Bytes of a stage: S operand hi (and lo), the tile as TMA brought it where it has to
@@ -132,7 +132,10 @@ struct GtShape {
   static constexpr int RAW = F16 ? 4 * GT_ATOM : 2 * GT_ATOM;
   static constexpr int WHI = RAW + (F16 ? 2 : 1) * GT_ATOM, WLO = WHI + W;
   static constexpr int STAGE = WLO + W;
-  static constexpr int S = F16 ? (RP > 64 ? 2 : 3) : (RP > 64 ? 3 : 5);
+  static constexpr int S = F16 ? (RP > 64 ? 2 : 3) : 4;
+  static constexpr int NG = F16 && RP <= 64 ? 3 : 2;  // groups of operand warps
+  static constexpr int THREADS = 64 + 128 * NG;
+  static_assert(S % NG == 0, "a slot belongs to one group");
   static constexpr int SUMS = RP * GT_LD * 4;
   static constexpr size_t SMEM = (size_t)S * STAGE + 256 + GT_TABLE * sizeof(LoraPiece);
   static_assert(SUMS <= S * STAGE && SMEM <= 232448, "shared memory of a CTA");
@@ -166,12 +169,12 @@ __device__ __forceinline__ uint4 gt_codes(uint32_t a, uint32_t b) {
 }
 
 template <int RP, bool F16>
-__global__ void __launch_bounds__(GT_THREADS, 1)
+__global__ void __launch_bounds__(GtShape<RP, F16>::THREADS, 1)
 lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                  LoraGradArgs ga, LoraGradArgs gb, LoraGradCommon c, int blocks_a, int split) {
   using Sh = GtShape<RP, F16>;
   using T = typename LoraType<!F16>::T;
-  constexpr int S = Sh::S;
+  constexpr int S = Sh::S, NG = Sh::NG, GT_THREADS = Sh::THREADS;
   extern __shared__ __align__(1024) uint8_t gt_smem[];
   uint64_t* bars = (uint64_t*)(gt_smem + S * Sh::STAGE);
   uint64_t* full = bars;            // [S] the tile landed
@@ -183,7 +186,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   volatile int* issued = abort_flag + 1;
   int* scan = (int*)(tmem_slot + 3);  // GT_THREADS / 32 + 1 ints
   LoraPiece* table = (LoraPiece*)(gt_smem + S * Sh::STAGE + 256);
-  static_assert((3 * S + 1) * 8 + 12 + 44 <= 256, "fits");
+  static_assert((3 * S + 1) * 8 + 12 + 4 * (GT_THREADS / 32 + 1) <= 256, "fits");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int part = (int)blockIdx.x % split, blk = (int)blockIdx.x / split;
@@ -262,7 +265,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
         }
       }
     } else {
-      // ---- operands: group `grp` of four warps takes every second tile ----
+      // ---- operands: group `grp` of four warps takes every NG-th tile ----
       const int grp = (warp - 2) / 4, gt = (warp - 2) % 4 * 32 + lane;
       constexpr int NCH = RP / 8;                 // 8-value chunks of a row of W
       constexpr int TASKS = GT_T * NCH / 128;     // chunks per thread
@@ -282,9 +285,9 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
           sc[k] = codes && have ? __ldg(g.s_scales + (int64_t)(p.t0 + t) * nb + col0 / 128) : 1.f;
         }
       };
-      int i = ((base & 1) == grp) ? 0 : 1;
+      int i = (grp - base % NG + NG) % NG;
       if (i < np) fetch(i);
-      for (; i < np; i += 2) {
+      for (; i < np; i += NG) {
         const int it = base + i, s = it % S;
         const int cnt = table[i].cnt;
         if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, c.spin)) break;
@@ -302,7 +305,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
           *reinterpret_cast<uint4*>(sb + Sh::WHI + o) = hi;
           *reinterpret_cast<uint4*>(sb + Sh::WLO + o) = lo;
         }
-        if (i + 2 < np) fetch(i + 2);
+        if (i + NG < np) fetch(i + NG);
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
         if (codes) {
 #pragma unroll
@@ -352,7 +355,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   tc::tc_fence_after();
   const bool ok = finished && !*abort_flag;
   float* sums = (float*)gt_smem;  // [RP][GT_LD]
-  if (warp >= 2) {
+  if (warp >= 2 && warp < 10) {
     const int quarter = warp & 3, hf = (warp - 2) / 4, col = quarter * 32 + lane;
     constexpr int HC = RP / 2, CW = HC < 32 ? HC : 32;
 #pragma unroll
@@ -441,7 +444,7 @@ gptq_status launch_grad(const LoraGradArgs& ga, const LoraGradArgs& gb, const Lo
   int split = 1;
   while (split < 8 && ctas * split * 2 <= sm_count() && tiles / (split * 2) >= 4) split *= 2;
   launch_cluster_pdl(lora_grad_kernel<RP, F16>, dim3((unsigned)((ba + bb) * split), (unsigned)c.na),
-                     dim3(GT_THREADS), Sh::SMEM, split, s, am, bm, ga, gb, c, ba, split);
+                     dim3(Sh::THREADS), Sh::SMEM, split, s, am, bm, ga, gb, c, ba, split);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }

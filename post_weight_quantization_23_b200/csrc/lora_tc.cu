@@ -419,12 +419,14 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           if ((g & 1) != grp) continue;
           const int s = it % S, b = g & 3;
           const int j0 = (rank + CS * q) * LT_N;
-          // the tile of Y, while the MMA runs
+          ok = tc::mbar_wait_warp(&d2_full[b], (uint32_t)(g / 4) & 1u, abort_flag, a.spin);
+          if (!ok) break;
+          // the MMA waited for the slot's copies, so this phase is over; the wait makes the
+          // tile of Y visible here.  (Before the MMA the slot might still be a phase behind,
+          // which the parity cannot tell from this one.)
           ok = tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin);
           if (!ok) break;
           uint8_t* ys = slot(s);
-          ok = tc::mbar_wait_warp(&d2_full[b], (uint32_t)(g / 4) & 1u, abort_flag, a.spin);
-          if (!ok) break;
           tc::tc_fence_after();
           float v[64];
           tc::tmem_ld_32x32b_x32(tmem + lanes + (uint32_t)(256 + 64 * b), v);

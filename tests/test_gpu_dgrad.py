@@ -155,3 +155,17 @@ def test_dgrad_empty_and_refusals():
                  lambda: quant_matmul_dgrad(y, *a, 4, 128, 256, out=torch.zeros(5, 256, device="cuda"))):
         with pytest.raises(GptqError):
             call()
+
+
+@pytest.mark.parametrize("n,k,m", [(2048, 2048, 700), (2048, 4096, 2048)])
+def test_dgrad_repeats_under_load(n, k, m):
+    # many calls back to back give the same bits (copies land in every order)
+    from post_weight_quantization_23_b200 import quant_matmul_dgrad
+    codes, scales, zeros, g_idx, dY, qw = _inputs(n, k, 4, 128, m, BF, False, 7)
+    a = (dY.cuda(), qw.cuda(), scales.cuda(), zeros.cuda(), 4, 128, k)
+    first = quant_matmul_dgrad(*a)
+    _check(first, dY, codes, scales, zeros, g_idx, BF, True)
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(500):
+        bad += (quant_matmul_dgrad(*a) != first).any()
+    assert int(bad) == 0

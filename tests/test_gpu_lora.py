@@ -367,3 +367,28 @@ def test_refusals():
                dict(dX=s["dX"][:, :8])):
         with pytest.raises(GptqError):
             back(**kw)
+
+
+@pytest.mark.parametrize("dtype,r", [(BF, 16), (BF, 64), (H, 16), (H, 128)])
+def test_repeats_under_load(dtype, r):
+    # many calls back to back give the same bits (copies land in every order)
+    from post_weight_quantization_23_b200 import act_checkpoint, lora_add, lora_backward
+    s = R.make(dtype, 2048, 2048, r, 2, [500, 300, 224], [0, 1, 0], r)
+    s["V"] = torch.zeros(1024, r, device="cuda")
+    a = (s["A"], s["B"], s["scaling"], s["starts"], s["adapter"])
+    out = torch.empty_like(s["Y"])
+    lora_add(s["Y"], s["X"], *a, out=out, V=s["V"])
+    first_y, V = out.clone(), s["V"].clone()
+    codes, xs = act_checkpoint(s["X"])
+    first = {}
+    for saved, (X, sc) in ((16, (s["X"], None)), (8, (codes, xs))):
+        o = torch.empty_like(s["dX"])
+        first[saved] = lora_backward(s["dY"], X, V, *a, s["dX"], x_scales=sc, out=o)
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        lora_add(s["Y"], s["X"], *a, out=out, V=s["V"])
+        saved, (X, sc) = ((16, (s["X"], None)), (8, (codes, xs)))[i % 2]
+        got = lora_backward(s["dY"], X, V, *a, s["dX"], x_scales=sc, out=torch.empty_like(s["dX"]))
+        for x, y in zip(got + (out, s["V"]), first[saved] + (first_y, V)):
+            bad += (x != y).any()
+    assert int(bad) == 0
