@@ -217,22 +217,25 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t id = tc::instr_desc(BF16 ? 1 : 0, 128, a.N, 1, 0);  // W MN-major, dY K-major
+      const uint32_t s0 = tc::smem_u32(dt_smem);
+      const uint64_t dw = tc::smem_desc_sw128(s0, 8192, 1024);
+      const uint64_t dy = tc::smem_desc_sw128(s0 + Sh::A, 16, 1024);
+      int s = 0;
+      uint32_t ph = 0;
       for (int it = 0; it < ns; ++it) {
-        const int s = it % S;
-        const uint32_t ph = (uint32_t)(it / S) & 1u;
         if (!tc::mbar_wait(&full[s], ph, abort_flag, a.spin)) break;
         if (!tc::mbar_wait(&ready[s], ph, abort_flag, a.spin)) break;
         tc::tc_fence_after();
-        const uint32_t sa = tc::smem_u32(stage(it)), sy = sa + Sh::A;
+        const uint64_t w = tc::desc_add(dw, (uint32_t)s * Sh::STAGE);
+        const uint64_t y = tc::desc_add(dy, (uint32_t)s * Sh::STAGE);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int kk = 0; kk < DT_K / 16; ++kk)
-            tc::mma_f16_ss(tmem + 256 * mt,
-                           tc::smem_desc_sw128(sa + mt * 16384 + kk * 2048, 8192, 1024),
-                           tc::smem_desc_sw128(sy + kk * 32, 16, 1024), id,
-                           (it > 0 || kk > 0) ? 1u : 0u);
+            tc::mma_f16_ss(tmem + 256 * mt, tc::desc_add(w, mt * 16384 + kk * 2048),
+                           tc::desc_add(y, kk * 32), id, kk > 0 ? 1u : (uint32_t)(it > 0));
         tc::mma_commit(&empty[s]);
+        if (++s == S) s = 0, ph ^= 1u;
       }
       tc::mma_commit(done);  // fires once every MMA issued above has finished
     }

@@ -243,25 +243,27 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
     } else if (warp == 1) {
       if (lane == 0) {
         const uint32_t id = tc::instr_desc(1, GT_C, RP, 1, 1);  // bf16, both MN-major
+        const uint64_t d0 = tc::smem_desc_sw128(tc::smem_u32(gt_smem), GT_ATOM, 1024);
+        const bool split_s = F16 && !codes;
+        int s = base % S;
+        uint32_t ph = (uint32_t)(base / S) & 1u;
         for (int i = 0; i < np; ++i) {
-          const int it = base + i, s = it % S;
-          const uint32_t ph = (uint32_t)(it / S) & 1u;
           if (!tc::mbar_wait(&full[s], ph, abort_flag, c.spin)) break;
           if (!tc::mbar_wait(&ready[s], ph, abort_flag, c.spin)) break;
           tc::tc_fence_after();
-          const uint32_t sb = tc::smem_u32(stage(it));
-          auto mma = [&](int x, int w, int kk, bool first) {
-            tc::mma_f16_ss(tmem, tc::smem_desc_sw128(sb + x + kk * 2048, GT_ATOM, 1024),
-                           tc::smem_desc_sw128(sb + w + kk * 2048, GT_ATOM, 1024), id,
-                           first ? 0u : 1u);
+          const uint64_t d = tc::desc_add(d0, (uint32_t)s * Sh::STAGE);
+          auto mma = [&](int x, int w, int kk, uint32_t acc) {
+            tc::mma_f16_ss(tmem, tc::desc_add(d, x + kk * 2048), tc::desc_add(d, w + kk * 2048), id,
+                           acc);
           };
 #pragma unroll
           for (int kk = 0; kk < GT_T / 16; ++kk) {
-            mma(Sh::HI, Sh::WLO, kk, it == 0 && kk == 0);
-            if (F16 && !codes) mma(Sh::LO, Sh::WHI, kk, false);
-            mma(Sh::HI, Sh::WHI, kk, false);
+            mma(Sh::HI, Sh::WLO, kk, kk > 0 ? 1u : (uint32_t)(base + i > 0));
+            if (split_s) mma(Sh::LO, Sh::WHI, kk, 1u);
+            mma(Sh::HI, Sh::WHI, kk, 1u);
           }
           tc::mma_commit(&empty[s]);
+          if (++s == S) s = 0, ph ^= 1u;
         }
       }
     } else {

@@ -230,54 +230,63 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       if (lane == 0) {
         const uint32_t id1 = tc::instr_desc(BF16 ? 1 : 0, LT_M, RP, 0, BWD ? 1 : 0);
         const uint32_t id2 = tc::instr_desc(BF16 ? 1 : 0, LT_M, LT_N, 0, BWD ? 1 : 0);
-        const int steps = (a.r + 15) / 16;  // 16-wide steps of the rank that hold values
-        const uint32_t sv = tc::smem_u32(opnd);
-        int it = base_it, g = base_g;
+        // descriptors of slot 0 and of the V operand
+        const uint32_t s0 = tc::smem_u32(lt_smem);
+        const uint64_t dx = tc::smem_desc_sw128(s0, 16, 1024);
+        const uint64_t dp = BWD ? tc::smem_desc_sw128(s0 + LT_TILE, 8192, 1024)
+                                : tc::smem_desc_sw128(s0 + LT_TILE, 16, 1024);
+        const uint64_t dv = tc::smem_desc_sw128(tc::smem_u32(opnd), 16, 1024);
+        int g = base_g, s = base_it % S;
+        uint32_t ph = (uint32_t)(base_it / S) & 1u;  // of the ring's current round
         bool ok = true;
+        auto advance = [&]() {
+          if (++s == S) s = 0, ph ^= 1u;
+        };
         auto reduce_mma = [&](int pi) {  // pi: running number of the piece
           const int b = pi & 1;
+          const uint32_t d1 = tmem + 128 * b;
           if (pi >= 2)
             ok = ok && tc::mbar_wait(&d1_empty[b], (uint32_t)(pi / 2 - 1) & 1u, abort_flag, a.spin);
           tc::tc_fence_after();
-          for (int i = 0; i < n1 && ok; ++i, ++it) {
-            const int s = it % S;
-            ok = tc::mbar_wait(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin);
+          for (int i = 0; i < n1 && ok; ++i) {
+            ok = tc::mbar_wait(&full[s], ph, abort_flag, a.spin);
             if (!ok) break;
             tc::tc_fence_after();
-            const uint32_t sx = tc::smem_u32(slot(s)), sp = sx + LT_TILE;
+            const uint32_t so = (uint32_t)s * Sh::STAGE;
+            const uint64_t x = tc::desc_add(dx, so), p = tc::desc_add(dp, so);
 #pragma unroll
             for (int kk = 0; kk < LT_K / 16; ++kk)
-              tc::mma_f16_ss(tmem + 128 * b, tc::smem_desc_sw128(sx + kk * 32, 16, 1024),
-                             BWD ? tc::smem_desc_sw128(sp + kk * 2048, 8192, 1024)
-                                 : tc::smem_desc_sw128(sp + kk * 32, 16, 1024),
-                             id1, (i > 0 || kk > 0) ? 1u : 0u);
+              tc::mma_f16_ss(d1, tc::desc_add(x, kk * 32), tc::desc_add(p, kk * (BWD ? 2048 : 32)),
+                             id1, kk > 0 ? 1u : (uint32_t)(i > 0));
 #pragma unroll
             for (int q = 0; q < 4; ++q) tc::mma_commit(&empty[s]);  // the barrier's four arrivals
+            advance();
           }
           if (ok) tc::mma_commit(&d1_full[b]);
         };
         auto output_mma = [&](int pi) {
           ok = ok && tc::mbar_wait(v_full, (uint32_t)pi & 1u, abort_flag, a.spin);
           tc::tc_fence_after();
-          for (int i = 0; i < nt && ok; ++i, ++it, ++g) {
-            const int s = it % S, b = g & 3;
+          for (int i = 0; i < nt && ok; ++i, ++g) {
+            const int b = g & 3;
+            const uint32_t d2 = tmem + 256 + 64 * b;
             if (g >= 4)
               ok = tc::mbar_wait(&d2_empty[b], (uint32_t)(g / 4 - 1) & 1u, abort_flag, a.spin);
-            ok = ok && tc::mbar_wait(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin);
+            ok = ok && tc::mbar_wait(&full[s], ph, abort_flag, a.spin);
             if (!ok) break;
             tc::tc_fence_after();
-            const uint32_t sq = tc::smem_u32(slot(s)) + LT_TILE;
-            for (int h = 1; h >= 0; --h)  // the low halves first
-              for (int p = 0; p < steps; ++p) {
+            const uint64_t q = tc::desc_add(dp, (uint32_t)s * Sh::STAGE);
+#pragma unroll
+            for (int h = 1; h >= 0; --h)  // the low halves first; columns past r are zeros
+#pragma unroll
+              for (int p = 0; p < RP / 16; ++p) {
                 const int kc = h * RP + p * 16;
-                tc::mma_f16_ss(
-                    tmem + 256 + 64 * b,
-                    tc::smem_desc_sw128(sv + (kc / 64) * LT_TILE + (kc % 64) * 2, 16, 1024),
-                    BWD ? tc::smem_desc_sw128(sq + p * 2048, 8192, 1024)
-                        : tc::smem_desc_sw128(sq + (p / 4) * 8192 + (p % 4) * 32, 16, 1024),
-                    id2, (h == 0 || p > 0) ? 1u : 0u);
+                tc::mma_f16_ss(d2, tc::desc_add(dv, (kc / 64) * LT_TILE + (kc % 64) * 2),
+                               tc::desc_add(q, BWD ? p * 2048 : (p / 4) * 8192 + (p % 4) * 32), id2,
+                               (h == 0 || p > 0) ? 1u : 0u);
               }
             tc::mma_commit(&d2_full[b]);
+            advance();
           }
           if (ok) tc::mma_commit(v_empty);
         };

@@ -294,6 +294,15 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   return d;
 }
 
+// The descriptor `bytes` further on (a multiple of 16; shared memory stays within the
+// 14 address bits, so nothing carries out of the field).  One thread issues every MMA,
+// and its integer work, not the tensor core, sets the pace of short MMAs: descriptors
+// are formed once and advanced by constants (128 x 64 x 16 MMAs issued from descriptors
+// built anew: 1830 cycles for eight).
+__device__ __forceinline__ uint64_t desc_add(uint64_t desc, uint32_t bytes) {
+  return desc + (uint64_t)(bytes >> 4);
+}
+
 // Instruction descriptor of kind::f16 / kind::tf32 with fp32 accumulation.
 // fmt: 0 = f16, 1 = bf16, 2 = tf32 (both operands the same type);
 // a_mn / b_mn: operand stored MN-major (1) or K-major (0).
