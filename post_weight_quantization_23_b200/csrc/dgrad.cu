@@ -215,7 +215,7 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (tc::elect_one()) {
       const uint32_t id = tc::instr_desc(BF16 ? 1 : 0, 128, a.N, 1, 0);  // W MN-major, dY K-major
       const uint32_t s0 = tc::smem_u32(dt_smem);
       const uint64_t dw = tc::smem_desc_sw128(s0, 8192, 1024);

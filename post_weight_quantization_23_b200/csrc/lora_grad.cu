@@ -241,7 +241,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
         }
       }
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint32_t id = tc::instr_desc(1, GT_C, RP, 1, 1);  // bf16, both MN-major
         const uint64_t d0 = tc::smem_desc_sw128(tc::smem_u32(gt_smem), GT_ATOM, 1024);
         const bool split_s = F16 && !codes;

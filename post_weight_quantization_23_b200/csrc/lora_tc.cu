@@ -79,8 +79,9 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   float* red = Sh::PIPE ? vbuf + Sh::VBUF / 4 : (float*)opnd;  // [CS][OWNED][RP]
   uint64_t* bars = (uint64_t*)(opnd + Sh::OPND + Sh::VBUF + Sh::RED);
   uint64_t* full = bars;              // [S] tiles landed
-  uint64_t* empty = bars + S;         // [S] slot free again
-  uint64_t* d1_full = bars + 2 * S;   // [2]
+  uint64_t* empty1 = bars + S;        // [S] the reduction's MMAs are done with the slot
+  uint64_t* empty2 = bars + 2 * S;    // [S] the epilogue is
+  uint64_t* d1_full = bars + 3 * S;   // [2]
   uint64_t* d1_empty = d1_full + 2;   // [2]
   uint64_t* x1 = d1_full + 4;         // partial sums of this CTA's rows arrived
   uint64_t* x2 = d1_full + 5;         // V of all rows arrived
@@ -96,14 +97,15 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   int* scan = (int*)(tmem_slot + 3);      // LT_THREADS / 32 + 1 ints
   LoraPiece* table = (LoraPiece*)(scan + 16);
   float* rowback = (float*)(table + LT_TABLE);  // f16: [2][128] factors to take back
-  static_assert((2 * S + 18) * 8 + 12 + 64 + LT_TABLE * sizeof(LoraPiece) + 1024 <= 2304, "fits");
+  static_assert((3 * S + 18) * 8 + 12 + 64 + LT_TABLE * sizeof(LoraPiece) + 1024 <= 2304, "fits");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], 4);
+      tc::mbar_init(&empty1[s], 1);
+      tc::mbar_init(&empty2[s], 4);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&d1_full[b], 1);
@@ -153,6 +155,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   // ring index of the first output tile of the i-th of n pieces, counted from the first
   // stage of this table; the pieces of earlier tables came before
   int base_it = 0, base_g = 0, base_p = 0;  // ring stages, output tiles, pieces so far
+  uint32_t tenant = 0, phase1 = 0, phase2 = 0;  // the producer's view of the slots
   auto first_tile = [&](int i, int n) {
     return base_it + n1 * (Sh::PIPE ? min(i + 2, n) : i + 1) + nt * i;
   };
@@ -177,15 +180,24 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       if (lane == 0) {
         int it = base_it;
         bool ok = true;
-        auto take = [&]() {  // the next slot of the ring, empty
+        auto take = [&](uint32_t kind) {  // the next slot of the ring, empty; kind 1: output tile
           const int s = it % S;
-          if (it >= S)
-            ok = tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, a.spin);
+          const uint32_t bit = 1u << s;
+          if (it >= S) {  // who had it last says on which barrier to wait
+            if (tenant & bit) {
+              ok = tc::mbar_wait(&empty2[s], (phase2 & bit) != 0, abort_flag, a.spin);
+              phase2 ^= bit;
+            } else {
+              ok = tc::mbar_wait(&empty1[s], (phase1 & bit) != 0, abort_flag, a.spin);
+              phase1 ^= bit;
+            }
+          }
+          tenant = kind ? tenant | bit : tenant & ~bit;
           return s;
         };
         auto reduce_tiles = [&](const LoraPiece pc) {
           for (int i = 0; i < n1 && ok; ++i) {
-            const int s = take();
+            const int s = take(0);
             if (!ok) break;
             uint8_t* sb = slot(s);
             const int c = (rank + CS * i) * LT_K;
@@ -203,7 +215,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         };
         auto output_tiles = [&](const LoraPiece pc) {
           for (int i = 0; i < nt && ok; ++i) {
-            const int s = take();
+            const int s = take(1);
             if (!ok) break;
             uint8_t* sb = slot(s);
             const int j = (rank + CS * i) * LT_N;
@@ -227,7 +239,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         if (Sh::PIPE && n > 0) output_tiles(table[n - 1]);
       }
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint32_t id1 = tc::instr_desc(BF16 ? 1 : 0, LT_M, RP, 0, BWD ? 1 : 0);
         const uint32_t id2 = tc::instr_desc(BF16 ? 1 : 0, LT_M, LT_N, 0, BWD ? 1 : 0);
         // descriptors of slot 0 and of the V operand
@@ -258,8 +270,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             for (int kk = 0; kk < LT_K / 16; ++kk)
               tc::mma_f16_ss(d1, tc::desc_add(x, kk * 32), tc::desc_add(p, kk * (BWD ? 2048 : 32)),
                              id1, kk > 0 ? 1u : (uint32_t)(i > 0));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tc::mma_commit(&empty[s]);  // the barrier's four arrivals
+            tc::mma_commit(&empty1[s]);
             advance();
           }
           if (ok) tc::mma_commit(&d1_full[b]);
@@ -437,53 +448,60 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           if (!ok) break;
           uint8_t* ys = slot(s);
           tc::tc_fence_after();
-          float v[64];
-          tc::tmem_ld_32x32b_x32(tmem + lanes + (uint32_t)(256 + 64 * b), v);
-          tc::tmem_ld_32x32b_x32(tmem + lanes + (uint32_t)(256 + 64 * b + 32), v + 32);
-          uint4 yv[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            yv[c] = a.Y != nullptr
-                        ? *reinterpret_cast<const uint4*>(ys + row * 128 + ((c ^ (row & 7)) << 4))
-                        : make_uint4(0u, 0u, 0u, 0u);
-          tc::tmem_ld_wait();
+          for (int h = 0; h < 2; ++h) {  // 32 columns at a time
+            float v[32];
+            tc::tmem_ld_32x32b_x32(tmem + lanes + (uint32_t)(256 + 64 * b + 32 * h), v);
+            uint4 yv[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              yv[c] = a.Y != nullptr ? *reinterpret_cast<const uint4*>(
+                                           ys + row * 128 + (((4 * h + c) ^ (row & 7)) << 4))
+                                     : make_uint4(0u, 0u, 0u, 0u);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[4] = {yv[c].x, yv[c].y, yv[c].z, yv[c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 y = Ty::unpack(w[e]);
+                w[e] = Ty::pack(fmaf(v[8 * c + 2 * e], back, y.x),
+                                fmaf(v[8 * c + 2 * e + 1], back, y.y));
+              }
+              *reinterpret_cast<uint4*>(ys + row * 128 + (((4 * h + c) ^ (row & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
           tc::tc_fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&d2_empty[b]);
+          // this warp's 32 rows, 128 contiguous bytes per row; all reads before the first store
+          const int c = lane % 8, j = j0 + 8 * c, r0 = quarter * 32 + lane / 8;
+          uint4 w[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t w[4] = {yv[c].x, yv[c].y, yv[c].z, yv[c].w};
+          for (int e = 0; e < 8; ++e)
+            w[e] = *reinterpret_cast<const uint4*>(ys + (r0 + 4 * e) * 128 +
+                                                   ((c ^ ((r0 + 4 * e) & 7)) << 4));
+          T* o = out + (int64_t)(pc.t0 + r0) * a.ldo + j;
+          if (ovec && j + 8 <= a.N) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 y = Ty::unpack(w[e]);
-              w[e] = Ty::pack(fmaf(v[8 * c + 2 * e], back, y.x),
-                              fmaf(v[8 * c + 2 * e + 1], back, y.y));
-            }
-            *reinterpret_cast<uint4*>(ys + row * 128 + ((c ^ (row & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          __syncwarp();
-          // this warp's 32 rows, 128 contiguous bytes per row
-          const int c = lane % 8, j = j0 + 8 * c;
+            for (int e = 0; e < 8; ++e)
+              if (r0 + 4 * e < pc.cnt) *reinterpret_cast<uint4*>(o + (int64_t)(4 * e) * a.ldo) = w[e];
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int r = quarter * 32 + 4 * e + lane / 8;
-            if (r >= pc.cnt || j >= a.N) continue;
-            const uint4 w = *reinterpret_cast<const uint4*>(ys + r * 128 + ((c ^ (r & 7)) << 4));
-            T* o = out + (int64_t)(pc.t0 + r) * a.ldo + j;
-            if (ovec && j + 8 <= a.N) {
-              *reinterpret_cast<uint4*>(o) = w;
-            } else {
-              const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            for (int e = 0; e < 8; ++e) {
+              if (r0 + 4 * e >= pc.cnt) continue;
+              const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
 #pragma unroll
               for (int x = 0; x < 8; ++x)
                 if (j + x < a.N)
-                  reinterpret_cast<unsigned short*>(o)[x] = (unsigned short)(u[x / 2] >> (16 * (x % 2)));
+                  reinterpret_cast<unsigned short*>(o + (int64_t)(4 * e) * a.ldo)[x] =
+                      (unsigned short)(u[x / 2] >> (16 * (x % 2)));
             }
           }
           tc::fence_proxy_async_smem();  // the next copy into the slot comes after these accesses
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&empty[s]);
+          if (lane == 0) tc::mbar_arrive(&empty2[s]);
         }
       }
     }
