@@ -30,22 +30,67 @@ constexpr int A8_UNROLL = 4;       // vectors in flight per thread
 // must stay finite)
 constexpr float A8_TINY = 7.8886090522101181e-31f;  // 2^-100
 
+// Division by a fixed number below 2^31 as a multiplication: n / d for n < 2^31.
+struct A8Div {
+  uint32_t mul, shift;
+};
+A8Div a8_div(uint32_t d) {
+  A8Div r;
+  r.shift = 0;
+  while (((uint64_t)1 << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << r.shift) - d)) / d + 1);
+  return r;
+}
+__device__ __forceinline__ uint32_t a8_quot(uint32_t n, A8Div d) {
+  return (__umulhi(d.mul, n) + n) >> d.shift;
+}
+
+// Eight columns as they lie in memory; columns past `have` are zeros.
+template <typename T> struct A8Raw { uint32_t w[sizeof(T) * 2]; };
+
 template <typename T>
-__device__ __forceinline__ void a8_load(const T* __restrict__ p, int have, bool vec, float (&x)[8]) {
+__device__ __forceinline__ A8Raw<T> a8_load(const T* __restrict__ p, int have, bool vec) {
+  A8Raw<T> r;
   if (vec && have == A8_VEC) {
-    if (sizeof(T) == 2) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const T* h = reinterpret_cast<const T*>(&u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = to_f32(h[i]);
-    } else {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      reinterpret_cast<uint4*>(r.w)[i] = reinterpret_cast<const uint4*>(p)[i];
   } else {
+    T v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = i < have ? to_f32(p[i]) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = i < have ? p[i] : T(0.f);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) * 2; ++i) r.w[i] = reinterpret_cast<const uint32_t*>(v)[i];
   }
+  return r;
+}
+
+// The bits of the largest |x| of 128 columns (16 lanes), as fp32; a NaN is above infinity.
+// 16-bit types are compared two at a time as integers, which order like the magnitudes.
+template <typename T>
+__device__ __forceinline__ uint32_t a8_top(const A8Raw<T>& r) {
+  if (sizeof(T) == 4) {
+    uint32_t t = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, r.w[i] & 0x7fffffffu);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+    return t;
+  }
+  uint32_t t = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t = __vmaxu2(t, r.w[i] & 0x7fff7fffu);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+  const unsigned short h = (unsigned short)max(t & 0xffffu, t >> 16);
+  return __float_as_uint(to_f32(*reinterpret_cast<const T*>(&h)));
+}
+
+template <typename T>
+__device__ __forceinline__ float a8_value(const A8Raw<T>& r, int i) {
+  if (sizeof(T) == 4) return __uint_as_float(r.w[i]);
+  const unsigned short h = (unsigned short)(r.w[i / 2] >> (16 * (i % 2)));
+  return to_f32(*reinterpret_cast<const T*>(&h));
 }
 
 template <typename T> __device__ __forceinline__ T a8_out(float v);
@@ -55,61 +100,70 @@ template <> __device__ __forceinline__ __nv_bfloat16 a8_out<__nv_bfloat16>(float
   return __float2bfloat16_rn(v);
 }
 
-// rows of X from row 0; nvp = vectors per row rounded up to whole blocks
+// rows of X from row 0; nvp = vectors per row rounded up to whole blocks.  The two
+// divisions of a block are done once: of a thread's four vectors, lane l takes those of
+// vector l % 4 and hands the factor round.
 template <typename T>
 __global__ void __launch_bounds__(A8_THREADS)
-act_checkpoint_kernel(const T* __restrict__ X, int64_t ldx, uint32_t total, uint32_t nvp, int k,
-                      int nb, int xvec, int cvec, int8_t* __restrict__ codes, int64_t ldc,
+act_checkpoint_kernel(const T* __restrict__ X, int64_t ldx, uint32_t total, uint32_t nvp, A8Div div,
+                      int k, int nb, int xvec, int cvec, int8_t* __restrict__ codes, int64_t ldc,
                       float* __restrict__ scales) {
+  static_assert(A8_UNROLL == 4, "a lane per vector");
   pdl_wait();
   pdl_trigger();
   const uint32_t base = blockIdx.x * (A8_THREADS * A8_UNROLL) + threadIdx.x;
-  float x[A8_UNROLL][8];
-  uint32_t row[A8_UNROLL];
-  int col[A8_UNROLL];
+  const int lane = threadIdx.x & 31;
+  A8Raw<T> x[A8_UNROLL];
+  uint32_t row[A8_UNROLL], top[A8_UNROLL];
+  int col[A8_UNROLL], have[A8_UNROLL];
 #pragma unroll
   for (int u = 0; u < A8_UNROLL; ++u) {
     const uint32_t e = base + u * A8_THREADS;
-    row[u] = e / nvp;
+    row[u] = a8_quot(e, div);
     col[u] = (int)(e - row[u] * nvp) * A8_VEC;
-    const int have = e < total ? min(max(k - col[u], 0), A8_VEC) : 0;
-    a8_load(X + (int64_t)row[u] * ldx + col[u], have, xvec != 0, x[u]);
+    have[u] = e < total ? min(max(k - col[u], 0), A8_VEC) : 0;
+    x[u] = a8_load(X + (int64_t)row[u] * ldx + col[u], have[u], xvec != 0);
+  }
+#pragma unroll
+  for (int u = 0; u < A8_UNROLL; ++u) top[u] = a8_top(x[u]);
+  float inv;
+  {
+    const int u = lane & 3;
+    const uint32_t t = u == 0 ? top[0] : u == 1 ? top[1] : u == 2 ? top[2] : top[3];
+    const uint32_t r = u == 0 ? row[0] : u == 1 ? row[1] : u == 2 ? row[2] : row[3];
+    const int c = u == 0 ? col[0] : u == 1 ? col[1] : u == 2 ? col[2] : col[3];
+    const float f = __uint_as_float(t);
+    const bool bad = t >= 0x7f800000u, tiny = f < A8_TINY;  // bad: NaN or infinity in the block
+    inv = (bad || tiny) ? 0.f : __fdiv_rn(127.f, f);
+    const float scale = bad ? __uint_as_float(0x7fc00000u) : tiny ? 0.f : __fdiv_rn(f, 127.f);
+    if ((lane & 15) < 4 && base + u * A8_THREADS < total)
+      scales[(int64_t)r * nb + c / A8_BLOCK] = scale;
   }
 #pragma unroll
   for (int u = 0; u < A8_UNROLL; ++u) {
-    const uint32_t e = base + u * A8_THREADS;
-    // the largest |x| by its bits, in which a NaN is above infinity
-    uint32_t top = 0u;
+    const float f = __shfl_sync(0xffffffffu, inv, (lane & ~3) | u);
+    uint32_t q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[u][i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(__fmaf_rn(a8_value(x[u], i), f, 12582912.f));
+    uint32_t w[2];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float t = __uint_as_float(top);
-    const bool bad = top >= 0x7f800000u, tiny = t < A8_TINY;  // bad: NaN or infinity in the block
-    const float inv = (bad || tiny) ? 0.f : __fdiv_rn(127.f, t);
-    const float scale = bad ? __uint_as_float(0x7fc00000u) : tiny ? 0.f : __fdiv_rn(t, 127.f);
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t q = bad ? 0u : __float_as_uint(__fmaf_rn(x[u][i], inv, 12582912.f));
-      w[i / 4] |= (q & 0xFFu) << (8 * (i % 4));
-    }
-    if (e >= total) continue;
-    const int have = min(max(k - col[u], 0), A8_VEC);
+    for (int i = 0; i < 2; ++i)  // the low bytes
+      w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040),
+                         __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
+    if (top[u] >= 0x7f800000u) w[0] = w[1] = 0u;
     int8_t* dst = codes + (int64_t)row[u] * ldc + col[u];
-    if (cvec && have == A8_VEC) {
+    if (cvec && have[u] == A8_VEC) {
       *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     } else {
-      for (int i = 0; i < have; ++i) dst[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+      for (int i = 0; i < have[u]; ++i) dst[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
     }
-    if (col[u] % A8_BLOCK == 0) scales[(int64_t)row[u] * nb + col[u] / A8_BLOCK] = scale;
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(A8_THREADS)
 act_restore_kernel(const int8_t* __restrict__ codes, int64_t ldc, const float* __restrict__ scales,
-                   uint32_t total, uint32_t nvp, int k, int nb, int cvec, int ovec,
+                   uint32_t total, uint32_t nvp, A8Div div, int k, int nb, int cvec, int ovec,
                    T* __restrict__ out, int64_t ldo) {
   pdl_wait();
   pdl_trigger();
@@ -121,7 +175,7 @@ act_restore_kernel(const int8_t* __restrict__ codes, int64_t ldc, const float* _
 #pragma unroll
   for (int u = 0; u < A8_UNROLL; ++u) {
     const uint32_t e = base + u * A8_THREADS;
-    row[u] = e / nvp;
+    row[u] = a8_quot(e, div);
     col[u] = (int)(e - row[u] * nvp) * A8_VEC;
     const int have = e < total ? min(max(k - col[u], 0), A8_VEC) : 0;
     const int8_t* p = codes + (int64_t)row[u] * ldc + col[u];
@@ -182,8 +236,8 @@ gptq_status checkpoint_typed(const T* X, int64_t m, int64_t k, int64_t ldx, int8
   for (int64_t r0 = 0; r0 < m; r0 += step) {
     const int64_t rows = std::min(step, m - r0), total = rows * nvp;
     launch_pdl(act_checkpoint_kernel<T>, dim3((unsigned)cdiv(total, A8_THREADS * A8_UNROLL)),
-               dim3(A8_THREADS), 0, s, X + r0 * ldx, ldx, (uint32_t)total, (uint32_t)nvp, (int)k,
-               (int)nb, xvec, cvec, codes + r0 * ldc, ldc, scales + r0 * nb);
+               dim3(A8_THREADS), 0, s, X + r0 * ldx, ldx, (uint32_t)total, (uint32_t)nvp,
+               a8_div((uint32_t)nvp), (int)k, (int)nb, xvec, cvec, codes + r0 * ldc, ldc, scales + r0 * nb);
     GPTQ_CHECK_LAUNCH();
   }
   return GPTQ_OK;
@@ -200,7 +254,7 @@ gptq_status restore_typed(const int8_t* codes, int64_t ldc, const float* scales,
     const int64_t rows = std::min(step, m - r0), total = rows * nvp;
     launch_pdl(act_restore_kernel<T>, dim3((unsigned)cdiv(total, A8_THREADS * A8_UNROLL)),
                dim3(A8_THREADS), 0, s, codes + r0 * ldc, ldc, scales + r0 * nb, (uint32_t)total,
-               (uint32_t)nvp, (int)k, (int)nb, cvec, ovec, out + r0 * ldo, ldo);
+               (uint32_t)nvp, a8_div((uint32_t)nvp), (int)k, (int)nb, cvec, ovec, out + r0 * ldo, ldo);
     GPTQ_CHECK_LAUNCH();
   }
   return GPTQ_OK;

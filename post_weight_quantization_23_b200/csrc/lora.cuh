@@ -202,6 +202,12 @@ __device__ __forceinline__ void lora_split(float a, float b, uint32_t& hi, uint3
   lo = Ty::pack(la, lb);
 }
 
+// The same for bf16 without the look at hi: a value that is not finite in bf16 gives NaN.
+__device__ __forceinline__ void lora_split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = LoraType<true>::pack(a, b);
+  lo = LoraType<true>::pack(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
+
 // f16 only: the power of two that brings a row whose largest magnitude is `top`
 // to [2^7, 2^8), where neither half of the split leaves f16's range; 1 for a
 // zero or non-finite row.  Exact to apply and to take back.

@@ -133,7 +133,8 @@ struct GtShape {
   static constexpr int WHI = RAW + (F16 ? 2 : 1) * GT_ATOM, WLO = WHI + W;
   static constexpr int STAGE = WLO + W;
   static constexpr int S = F16 ? (RP > 64 ? 2 : 3) : 4;
-  static constexpr int NG = F16 && RP <= 64 ? 3 : 2;  // groups of operand warps
+  // groups of operand warps: as many as stages, where their registers allow it
+  static constexpr int NG = RP <= 64 ? S : 2;
   static constexpr int THREADS = 64 + 128 * NG;
   static_assert(S % NG == 0, "a slot belongs to one group");
   static constexpr int SUMS = RP * GT_LD * 4;
@@ -148,7 +149,7 @@ __device__ __forceinline__ void gt_split_f16(uint4 u, uint4& hi, uint4& lo) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = LoraType<false>::unpack(in[i]);
-    lora_split<true>(v.x, v.y, h[i], l[i]);
+    lora_split_bf16(v.x, v.y, h[i], l[i]);
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
@@ -299,10 +300,10 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
           const int e = gt + 128 * k, t = e / NCH, ch = e % NCH;
           const float f = sc[k];
           uint4 hi, lo;
-          lora_split<true>(w[k][0].x * f, w[k][0].y * f, hi.x, lo.x);
-          lora_split<true>(w[k][0].z * f, w[k][0].w * f, hi.y, lo.y);
-          lora_split<true>(w[k][1].x * f, w[k][1].y * f, hi.z, lo.z);
-          lora_split<true>(w[k][1].z * f, w[k][1].w * f, hi.w, lo.w);
+          lora_split_bf16(w[k][0].x * f, w[k][0].y * f, hi.x, lo.x);
+          lora_split_bf16(w[k][0].z * f, w[k][0].w * f, hi.y, lo.y);
+          lora_split_bf16(w[k][1].x * f, w[k][1].y * f, hi.z, lo.z);
+          lora_split_bf16(w[k][1].z * f, w[k][1].w * f, hi.w, lo.w);
           const int o = (ch / 8) * GT_ATOM + t * 128 + (((ch % 8) ^ (t & 7)) << 4);
           *reinterpret_cast<uint4*>(sb + Sh::WHI + o) = hi;
           *reinterpret_cast<uint4*>(sb + Sh::WLO + o) = lo;
