@@ -243,21 +243,24 @@ struct LoraArgs : LoraRequests {
   uint32_t spin;
 };
 
+constexpr int LORA_ANY = -1;
+
 // Pieces first, first + stride, .. (at most `cap`, from the `skip`-th of them) of
-// TT rows, of all requests or (only >= 0) of one adapter's, into `table`, by the
-// whole CTA; their number.  Each thread counts the
+// TT rows, of one adapter's requests (only >= 0) or of all that have an adapter
+// (LORA_ANY), into `table`, by the whole CTA; their number.  Each thread counts the
 // pieces of a run of requests, a scan locates them, and each thread writes those
 // of its run that are asked for.  `sm` holds NT / 32 + 1 ints.
 template <int NT>
 __device__ __forceinline__ int lora_find_pieces(const LoraRequests& a, int TT, int first,
                                                 int stride, int skip, LoraPiece* table, int cap,
-                                                int* sm, int only = -1) {
+                                                int* sm, int only) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.nreq + NT - 1) / NT;
   const int q0 = min(a.nreq, tid * per), q1 = min(a.nreq, q0 + per);
   int own = 0;
   auto pieces = [&](int q) {
-    return only >= 0 && a.adapter[q] != only
+    const int ad = a.adapter[q];
+    return (only >= 0 ? ad != only : ad < 0 || ad >= a.na)
                ? 0
                : lora_pieces(a.starts, q, a.m, TT, a.min_len, a.max_len);
   };
@@ -287,8 +290,7 @@ __device__ __forceinline__ int lora_find_pieces(const LoraRequests& a, int TT, i
         LoraPiece r;
         r.t0 = lora_clamp(a.starts[q], a.m) + (int)(p0 + i * stride - at) * TT;
         r.cnt = min(TT, lora_clamp(a.starts[q + 1], a.m) - r.t0);
-        const int ad = a.adapter[q];
-        r.a = ad < 0 || ad >= a.na ? -1 : ad;
+        r.a = a.adapter[q];
         table[i] = r;
       }
     }
@@ -329,6 +331,55 @@ __device__ __forceinline__ void lora_copy_piece(const LoraArgs& a, const LoraPie
   }
   if (a.V != nullptr && rank == 0)
     for (int e = threadIdx.x; e < pc.cnt * a.r; e += nthreads) a.V[(int64_t)pc.t0 * a.r + e] = 0.f;
+}
+
+// The same over the whole batch, for a launch whose pieces have adapters only: part
+// `part` of `nparts` takes every nparts-th row of every such request; `nthreads` (a
+// multiple of 32) threads of the CTA call it, thread `tid` of them.
+template <typename T>
+__device__ __forceinline__ void lora_copy_bare(const LoraArgs& a, int part, int nparts, int tid,
+                                               int nthreads, int vec) {
+  const bool rows = a.out != nullptr && a.Y != a.out;
+  if (!rows && a.V == nullptr) return;
+  const int lane = threadIdx.x & 31;
+  for (int q0 = 0; q0 < a.nreq; q0 += 32) {
+    const int q = q0 + lane;
+    bool bare = false;
+    if (q < a.nreq) {
+      const int ad = a.adapter[q];
+      bare = (ad < 0 || ad >= a.na) && lora_pieces(a.starts, q, a.m, 1, a.min_len, a.max_len) > 0;
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, bare); left != 0; left &= left - 1) {
+      const int r = q0 + __ffs(left) - 1;
+      const int b = lora_clamp(a.starts[r], a.m), e = lora_clamp(a.starts[r + 1], a.m);
+      const int mine = (e - b - part + nparts - 1) / nparts;  // rows b + part, + nparts, ..
+      if (mine <= 0) continue;
+      if (rows) {
+        const T* Y = (const T*)a.Y + (int64_t)(b + part) * a.ldy;
+        T* out = (T*)a.out + (int64_t)(b + part) * a.ldo;
+        for (int i = tid / 32; i < mine; i += nthreads / 32) {  // a row per warp
+          const T* y = Y + (int64_t)i * nparts * a.ldy;
+          T* o = out + (int64_t)i * nparts * a.ldo;
+#pragma unroll 8
+          for (int j = 8 * lane; j < a.N; j += 256) {
+            if (vec && j + 8 <= a.N) {
+              *reinterpret_cast<uint4*>(o + j) =
+                  a.Y != nullptr ? __ldg(reinterpret_cast<const uint4*>(y + j))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            } else {
+              for (int p = j; p < min(j + 8, a.N); ++p)
+                reinterpret_cast<unsigned short*>(o)[p] =
+                    a.Y != nullptr ? reinterpret_cast<const unsigned short*>(y)[p]
+                                   : (unsigned short)0;
+            }
+          }
+        }
+      }
+      if (a.V != nullptr)
+        for (int x = tid; x < mine * a.r; x += nthreads)
+          a.V[(int64_t)(b + part + (x / a.r) * nparts) * a.r + x % a.r] = 0.f;
+    }
+  }
 }
 
 }  // namespace gptq

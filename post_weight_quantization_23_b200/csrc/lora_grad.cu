@@ -16,6 +16,8 @@
 //     for f16's smallest subnormals), three products, lo x lo left out.
 //   S in 8-bit codes becomes bf16 exactly (|code| <= 127), and its scales, one per token
 //     and 128-column block, multiply the rows of W: the checkpoint is never restored.
+// Tiles to be converted land in a ring of their own, deeper than the operands' (a tile of
+// codes is 8 KB, and the way from its copy to its MMA is twice as long as a bf16 tile's).
 // Rows behind a request's end in its last tile belong to others (or hold anything):
 // both operands are zeroed there.
 // Warps: 0 TMA, 1 MMA, then the operand warps (groups of four, tile by tile in turn),
@@ -122,23 +124,27 @@ constexpr int GT_C = 128, GT_T = 64;         // columns and tokens of a tile
 constexpr int GT_ATOM = GT_T * 128;          // 64 tokens x 64 16-bit columns, 8 KB
 constexpr int GT_TABLE = 128;                // tiles looked up at a time
 constexpr int GT_LD = GT_C + 1;              // row stride of the staged sums (no bank conflicts)
+constexpr int GT_BARS = 384;                 // bytes of barriers and small words
 
-// Bytes of a stage: S operand hi (and lo), the tile as TMA brought it where it has to
-// be converted (bf16 arrives in place), W hi and lo.
+// A slot of the operand ring: S hi (and lo), W hi and lo.  Tiles to be converted (f16,
+// codes) land in RAW bytes behind the slots.
 template <int RP, bool F16>
 struct GtShape {
   static constexpr int W = (RP > 64 ? 2 : 1) * GT_ATOM;
   static constexpr int HI = 0, LO = 2 * GT_ATOM;
-  static constexpr int RAW = F16 ? 4 * GT_ATOM : 2 * GT_ATOM;
-  static constexpr int WHI = RAW + (F16 ? 2 : 1) * GT_ATOM, WLO = WHI + W;
+  static constexpr int WHI = (F16 ? 4 : 2) * GT_ATOM, WLO = WHI + W;
   static constexpr int STAGE = WLO + W;
   static constexpr int S = F16 ? (RP > 64 ? 2 : 3) : 4;
-  // groups of operand warps: as many as stages, where their registers allow it
+  // groups of operand warps: as many as slots, where their registers allow it
   static constexpr int NG = RP <= 64 ? S : 2;
+  static constexpr int RAW = (RP > 64 ? 4 : F16 ? 6 : 8) * GT_ATOM;
+  static constexpr int R_CODES = RAW / GT_ATOM, R_F16 = RAW / (2 * GT_ATOM);
   static constexpr int THREADS = 64 + 128 * NG;
-  static_assert(S % NG == 0, "a slot belongs to one group");
+  static_assert(S % NG == 0 && R_CODES % NG == 0 && (!F16 || R_F16 % NG == 0),
+                "a slot belongs to one group");
   static constexpr int SUMS = RP * GT_LD * 4;
-  static constexpr size_t SMEM = (size_t)S * STAGE + 256 + GT_TABLE * sizeof(LoraPiece);
+  static constexpr size_t SMEM =
+      (size_t)S * STAGE + RAW + GT_BARS + GT_TABLE * sizeof(LoraPiece);
   static_assert(SUMS <= S * STAGE && SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -155,18 +161,24 @@ __device__ __forceinline__ void gt_split_f16(uint4 u, uint4& hi, uint4& lo) {
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// Eight int8 codes as bf16, exactly: 2^23 + 2^7 + code in the low byte of a float.
-__device__ __forceinline__ uint4 gt_codes(uint32_t a, uint32_t b) {
-  uint32_t o[4];
+// Four int8 codes as bf16, exactly and two at a time: with the code's low seven bits in the
+// mantissa of 128 (128 + low) and its sign bit in that of another 128 (128 or 256), the
+// difference is the code.
+__device__ __forceinline__ uint2 gt_codes(uint32_t w) {
+  uint32_t o[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = (i < 2 ? a : b) ^ 0x80808080u;  // code + 128
-    const uint32_t s = 2 * (i % 2);
-    const float x = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | s)) - 8388736.f;
-    const float y = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u | (s + 1))) - 8388736.f;
-    o[i] = LoraType<true>::pack(x, y);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = __byte_perm(w, 0u, i == 0 ? 0x4140u : 0x4342u);
+    const uint32_t h = (v & 0x007f007fu) | 0x43004300u, z = (v & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&h),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&z));
+    o[i] = *reinterpret_cast<const uint32_t*>(&d);
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  return make_uint2(o[0], o[1]);
+}
+__device__ __forceinline__ uint4 gt_codes(uint32_t a, uint32_t b) {
+  const uint2 x = gt_codes(a), y = gt_codes(b);
+  return make_uint4(x.x, x.y, y.x, y.y);
 }
 
 template <int RP, bool F16>
@@ -177,17 +189,19 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   using T = typename LoraType<!F16>::T;
   constexpr int S = Sh::S, NG = Sh::NG, GT_THREADS = Sh::THREADS;
   extern __shared__ __align__(1024) uint8_t gt_smem[];
-  uint64_t* bars = (uint64_t*)(gt_smem + S * Sh::STAGE);
-  uint64_t* full = bars;            // [S] the tile landed
-  uint64_t* ready = bars + S;       // [S] both operands are written
-  uint64_t* empty = bars + 2 * S;   // [S] the MMAs that read them are done
-  uint64_t* done = bars + 3 * S;
+  uint8_t* raws = gt_smem + S * Sh::STAGE;
+  uint64_t* bars = (uint64_t*)(raws + Sh::RAW);
+  uint64_t* full = bars;            // [8] the tile landed (in a slot, or in the raw ring)
+  uint64_t* rawfree = bars + 8;     // [8] the raw tile is converted
+  uint64_t* ready = bars + 16;      // [S] both operands are written
+  uint64_t* empty = ready + S;      // [S] the MMAs that read them are done
+  uint64_t* done = empty + S;
   uint32_t* tmem_slot = (uint32_t*)(done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;
   int* scan = (int*)(tmem_slot + 3);  // GT_THREADS / 32 + 1 ints
-  LoraPiece* table = (LoraPiece*)(gt_smem + S * Sh::STAGE + 256);
-  static_assert((3 * S + 1) * 8 + 12 + 4 * (GT_THREADS / 32 + 1) <= 256, "fits");
+  LoraPiece* table = (LoraPiece*)(raws + Sh::RAW + GT_BARS);
+  static_assert((16 + 2 * S + 1) * 8 + 12 + 4 * (GT_THREADS / 32 + 1) <= GT_BARS, "fits");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int part = (int)blockIdx.x % split, blk = (int)blockIdx.x / split;
@@ -196,10 +210,16 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   const CUtensorMap* map = second ? &bmap : &amap;
   const int col0 = (second ? blk - blocks_a : blk) * GT_C, ad = blockIdx.y;
   const bool codes = g.s_scales != nullptr;
+  const bool convert = F16 || codes;
+  // slots that the copies go round
+  const int R = codes ? Sh::R_CODES : F16 ? Sh::R_F16 : S;
   constexpr int TM = RP < 32 ? 32 : RP;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < 8; ++s) {
       tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&rawfree[s], 4);
+    }
+    for (int s = 0; s < S; ++s) {
       tc::mbar_init(&ready[s], 4);
       tc::mbar_init(&empty[s], 1);
     }
@@ -223,20 +243,20 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   for (int chunk = 1; np > 0; ++chunk) {
     if (warp == 0) {
       if (lane == 0) {
+        uint64_t* free = convert ? rawfree : empty;
         for (int i = 0; i < np; ++i) {
-          const int it = base + i, s = it % S;
-          if (it >= S && !tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, c.spin))
+          const int it = base + i, q = it % R;
+          if (it >= R && !tc::mbar_wait(&free[q], (uint32_t)(it / R - 1) & 1u, abort_flag, c.spin))
             break;
-          uint8_t* sb = stage(it);
           const int t0 = table[i].t0;
           if (codes) {
-            tc::mbar_arrive_expect_tx(&full[s], GT_ATOM);
-            tc::tma_load_2d(sb + Sh::RAW, map, &full[s], col0, t0);
+            tc::mbar_arrive_expect_tx(&full[q], GT_ATOM);
+            tc::tma_load_2d(raws + q * GT_ATOM, map, &full[q], col0, t0);
           } else {
-            uint8_t* dst = sb + (F16 ? Sh::RAW : Sh::HI);
-            tc::mbar_arrive_expect_tx(&full[s], 2 * GT_ATOM);
-            tc::tma_load_2d(dst, map, &full[s], col0, t0);
-            tc::tma_load_2d(dst + GT_ATOM, map, &full[s], col0 + 64, t0);
+            uint8_t* dst = F16 ? raws + q * (2 * GT_ATOM) : stage(q) + Sh::HI;
+            tc::mbar_arrive_expect_tx(&full[q], 2 * GT_ATOM);
+            tc::tma_load_2d(dst, map, &full[q], col0, t0);
+            tc::tma_load_2d(dst + GT_ATOM, map, &full[q], col0 + 64, t0);
           }
           *issued = it + 1;
         }
@@ -249,7 +269,7 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
         int s = base % S;
         uint32_t ph = (uint32_t)(base / S) & 1u;
         for (int i = 0; i < np; ++i) {
-          if (!tc::mbar_wait(&full[s], ph, abort_flag, c.spin)) break;
+          // the operand warps waited for the copy before they arrived
           if (!tc::mbar_wait(&ready[s], ph, abort_flag, c.spin)) break;
           tc::tc_fence_after();
           const uint64_t d = tc::desc_add(d0, (uint32_t)s * Sh::STAGE);
@@ -291,10 +311,13 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
       int i = (grp - base % NG + NG) % NG;
       if (i < np) fetch(i);
       for (; i < np; i += NG) {
-        const int it = base + i, s = it % S;
+        const int it = base + i, s = it % S, q = it % R;
         const int cnt = table[i].cnt;
-        if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, c.spin)) break;
-        uint8_t* sb = stage(it);
+        if (!tc::mbar_wait_warp(&full[q], (uint32_t)(it / R) & 1u, abort_flag, c.spin)) break;
+        if (convert && it >= S &&
+            !tc::mbar_wait_warp(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, c.spin))
+          break;
+        uint8_t* sb = stage(s);
 #pragma unroll
         for (int k = 0; k < TASKS; ++k) {
           const int e = gt + 128 * k, t = e / NCH, ch = e % NCH;
@@ -314,13 +337,14 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // 16 codes each
             const int e = gt + 128 * k, t = e / 8, j = e % 8;
-            const uint4 q = *reinterpret_cast<const uint4*>(sb + Sh::RAW + t * 128 + 16 * j);
+            const uint4 u =
+                *reinterpret_cast<const uint4*>(raws + q * GT_ATOM + t * 128 + 16 * j);
             const bool have = t < cnt;
             uint8_t* row = sb + Sh::HI + (j / 4) * GT_ATOM + t * 128;
             const int ch = 2 * (j % 4);
-            *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = have ? gt_codes(q.x, q.y) : z;
+            *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = have ? gt_codes(u.x, u.y) : z;
             *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) =
-                have ? gt_codes(q.z, q.w) : z;
+                have ? gt_codes(u.z, u.w) : z;
           }
         } else if (F16) {
 #pragma unroll
@@ -328,7 +352,8 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
             const int e = gt + 128 * k;
             const bool have = (e % 512) / 8 < cnt;
             uint4 hi = z, lo = z;
-            if (have) gt_split_f16(*reinterpret_cast<const uint4*>(sb + Sh::RAW + 16 * e), hi, lo);
+            if (have)
+              gt_split_f16(*reinterpret_cast<const uint4*>(raws + q * (2 * GT_ATOM) + 16 * e), hi, lo);
             *reinterpret_cast<uint4*>(sb + Sh::HI + 16 * e) = hi;
             *reinterpret_cast<uint4*>(sb + Sh::LO + 16 * e) = lo;
           }
@@ -338,7 +363,10 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
         }
         tc::fence_proxy_async_smem();  // the MMA reads what this thread wrote
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&ready[s]);
+        if (lane == 0) {
+          tc::mbar_arrive(&ready[s]);
+          if (convert) tc::mbar_arrive(&rawfree[q]);
+        }
       }
     }
     __syncthreads();
@@ -351,9 +379,9 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   if (warp == 1 && lane == 0) tc::mma_commit(done);
   const bool finished = tc::mbar_wait_warp(done, 0, abort_flag, tc::kSpinLimit);
   if (*abort_flag && threadIdx.x == 0)
-    for (int p = max(0, *issued - S); p < *issued; ++p)
+    for (int p = max(0, *issued - R); p < *issued; ++p)
       for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
-        if (tc::mbar_try_wait(&full[p % S], (uint32_t)(p / S) & 1u)) break;
+        if (tc::mbar_try_wait(&full[p % R], (uint32_t)(p / R) & 1u)) break;
   __syncthreads();
   tc::tc_fence_after();
   const bool ok = finished && !*abort_flag;

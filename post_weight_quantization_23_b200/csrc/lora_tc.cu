@@ -129,6 +129,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     tc::prefetch_tensormap(&qmap);
     tc::prefetch_tensormap(&ymap);
   }
+  __syncthreads();
+  cluster_arrive();  // this CTA runs and its barriers are set up
   pdl_wait();
   pdl_trigger();
   T* out = (T*)a.out;
@@ -142,13 +144,16 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   // without the pipeline the partial sums come where the operand is: one piece at a time,
   // a cluster barrier between two
   constexpr int CAP = Sh::PIPE ? LT_TABLE : 1;
-  int np = lora_find_pieces<LT_THREADS>(a, LT_M, cid, stride, 0, table, CAP, scan);
-  if (np == 0) return;  // the same for the whole cluster
+  int np = lora_find_pieces<LT_THREADS>(a, LT_M, cid, stride, 0, table, CAP, scan, LORA_ANY);
+  if (np == 0) {  // the same for the whole cluster
+    lora_copy_bare<T>(a, (int)blockIdx.x, (int)gridDim.x, threadIdx.x, LT_THREADS, ovec);
+    cluster_wait();
+    return;
+  }
   if (warp == 1) tc::tmem_alloc(tmem_slot, LT_TMEM);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  cluster_arrive();  // every CTA of the cluster runs and its barriers are set up
   cluster_wait();
   const uint32_t tmem = *tmem_slot;
   auto slot = [&](int s) { return lt_smem + (size_t)s * Sh::STAGE; };
@@ -160,22 +165,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     return base_it + n1 * (Sh::PIPE ? min(i + 2, n) : i + 1) + nt * i;
   };
   for (int chunk = 0;; ++chunk) {
-    // pieces without an adapter are copies; the others move up in the table
-    int n = 0;
-    for (int i = 0; i < np; ++i) {
-      const LoraPiece pc = table[i];
-      if (pc.a < 0) lora_copy_piece<T>(a, pc, rank, CS, LT_THREADS, ovec);
-      else ++n;
-    }
-    if (n < np) {
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int w = 0;
-        for (int i = 0; i < np; ++i)
-          if (table[i].a >= 0) table[w++] = table[i];
-      }
-      __syncthreads();
-    }
+    int n = np;
     if (warp == 0) {
       if (lane == 0) {
         int it = base_it;
@@ -424,6 +414,10 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       const int grp = (warp - 2 - LT_XCH) / 4;
       const int quarter = warp & 3, row = quarter * 32 + lane;
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      // rows without an adapter are copied while the first piece is reduced
+      if (chunk == 0)
+        lora_copy_bare<T>(a, (int)blockIdx.x, (int)gridDim.x, threadIdx.x - 64 - 32 * LT_XCH,
+                          32 * LT_EPI, ovec);
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         const int pi = base_p + i;
@@ -528,7 +522,6 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       for (;;) {
         for (int i = 0; i < n; ++i) {
           const LoraPiece pc = table[i];
-          if (pc.a < 0) continue;
           for (int e = warp; e < pc.cnt; e += LT_THREADS / 32) {
             const int64_t r = pc.t0 + e;
             for (int q = 0; q < nt; ++q)
@@ -541,7 +534,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         }
         ++chunk;
         __syncthreads();
-        n = lora_find_pieces<LT_THREADS>(a, LT_M, cid, stride, chunk * CAP, table, CAP, scan);
+        n = lora_find_pieces<LT_THREADS>(a, LT_M, cid, stride, chunk * CAP, table, CAP, scan, LORA_ANY);
         if (n == 0) break;
       }
       break;
@@ -551,7 +544,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     base_p += n;
     if (np < CAP) break;
     np = lora_find_pieces<LT_THREADS>(a, LT_M, cid, stride, (chunk + 1) * CAP, table, CAP,
-                                      scan);
+                                      scan, LORA_ANY);
     if (np == 0) break;
   }
   __syncthreads();
