@@ -300,33 +300,47 @@ __device__ __forceinline__ int lora_find_pieces(const LoraRequests& a, int TT, i
   return (int)n;
 }
 
+// Columns [j0, j1) of a row from y (zeros if NULL) to o by one warp; eight vectors are
+// loaded before the first is stored (the two might be the same memory, so the compiler
+// keeps loads behind stores: one vector at a time waits for HBM each time).
+template <typename T>
+__device__ __forceinline__ void lora_copy_row(const T* y, T* o, int j0, int j1, int vec) {
+  const int lane = threadIdx.x & 31;
+  if (vec) {
+    for (int b = j0; b < j1; b += 8 * 256) {
+      uint4 w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int j = b + 256 * q + 8 * lane;
+        w[q] = y != nullptr && j + 8 <= j1 ? *reinterpret_cast<const uint4*>(y + j)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int j = b + 256 * q + 8 * lane;
+        if (j + 8 <= j1) *reinterpret_cast<uint4*>(o + j) = w[q];
+      }
+    }
+    j0 = j1 - j1 % 8;  // j0 and vectors are multiples of 8
+  }
+  for (int j = j0 + lane; j < j1; j += 32)
+    reinterpret_cast<unsigned short*>(o)[j] =
+        y != nullptr ? reinterpret_cast<const unsigned short*>(y)[j] : (unsigned short)0;
+}
+
 // The rows of a request without an adapter: out = Y (0 without Y) unless they are
-// the same, V = 0.  CTA `rank` of `nctas` takes every nctas-th 64-column run of all
-// rows; `vec`: rows of Y and out start on 16-byte boundaries.
+// the same, V = 0.  CTA `rank` of `nctas` takes its share of the columns, warp by warp a
+// row; `vec`: rows of Y and out start on 16-byte boundaries.
 template <typename T>
 __device__ __forceinline__ void lora_copy_piece(const LoraArgs& a, const LoraPiece& pc, int rank,
                                                 int nctas, int nthreads, int vec) {
-  const T* Y = (const T*)a.Y;
-  T* out = (T*)a.out;
-  if (out != nullptr && a.Y != a.out) {
-    const int runs = (a.N + 63) / 64;
-    const int mine = runs <= rank ? 0 : (runs - rank + nctas - 1) / nctas;
-    const int total = pc.cnt * mine * 8;  // vectors of 8 values
-#pragma unroll 4
-    for (int e = threadIdx.x; e < total; e += nthreads) {
-      const int v = e % 8, run = (e / 8) % mine, i = e / (8 * mine);
-      const int j = (rank + nctas * run) * 64 + 8 * v;
+  if (a.out != nullptr && a.Y != a.out) {
+    const int per = ((a.N + nctas - 1) / nctas + 7) / 8 * 8;
+    const int j0 = min(a.N, rank * per), j1 = min(a.N, j0 + per);
+    for (int i = threadIdx.x / 32; i < pc.cnt; i += nthreads / 32) {
       const int64_t row = pc.t0 + i;
-      const T* y = Y + row * a.ldy + j;
-      T* o = out + row * a.ldo + j;
-      if (vec && j + 8 <= a.N) {
-        *reinterpret_cast<uint4*>(o) =
-            Y != nullptr ? *reinterpret_cast<const uint4*>(y) : make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        for (int q = 0; q < 8 && j + q < a.N; ++q)
-          reinterpret_cast<unsigned short*>(o)[q] =
-              Y != nullptr ? reinterpret_cast<const unsigned short*>(y)[q] : (unsigned short)0;
-      }
+      lora_copy_row<T>(a.Y != nullptr ? (const T*)a.Y + row * a.ldy : nullptr,
+                       (T*)a.out + row * a.ldo, j0, j1, vec);
     }
   }
   if (a.V != nullptr && rank == 0)
@@ -355,24 +369,10 @@ __device__ __forceinline__ void lora_copy_bare(const LoraArgs& a, int part, int 
       const int mine = (e - b - part + nparts - 1) / nparts;  // rows b + part, + nparts, ..
       if (mine <= 0) continue;
       if (rows) {
-        const T* Y = (const T*)a.Y + (int64_t)(b + part) * a.ldy;
-        T* out = (T*)a.out + (int64_t)(b + part) * a.ldo;
         for (int i = tid / 32; i < mine; i += nthreads / 32) {  // a row per warp
-          const T* y = Y + (int64_t)i * nparts * a.ldy;
-          T* o = out + (int64_t)i * nparts * a.ldo;
-#pragma unroll 8
-          for (int j = 8 * lane; j < a.N; j += 256) {
-            if (vec && j + 8 <= a.N) {
-              *reinterpret_cast<uint4*>(o + j) =
-                  a.Y != nullptr ? __ldg(reinterpret_cast<const uint4*>(y + j))
-                                 : make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              for (int p = j; p < min(j + 8, a.N); ++p)
-                reinterpret_cast<unsigned short*>(o)[p] =
-                    a.Y != nullptr ? reinterpret_cast<const unsigned short*>(y)[p]
-                                   : (unsigned short)0;
-            }
-          }
+          const int64_t row = b + part + (int64_t)i * nparts;
+          lora_copy_row<T>(a.Y != nullptr ? (const T*)a.Y + row * a.ldy : nullptr,
+                           (T*)a.out + row * a.ldo, 0, a.N, vec);
         }
       }
       if (a.V != nullptr)
