@@ -29,63 +29,6 @@ __device__ __forceinline__ int lora_pieces(const int32_t* starts, int q, int m, 
   return (len < min_len || len > max_len || len <= 0) ? 0 : (len + TT - 1) / TT;
 }
 
-// The `piece`-th piece over all requests, found by the whole CTA (NT threads, a
-// multiple of 32): each thread counts the pieces of a run of
-// requests, a scan over the threads locates the run, its thread walks it.
-// `sm` holds NT / 32 + 3 ints.
-template <int NT>
-__device__ __forceinline__ LoraPiece lora_find_piece(const int32_t* __restrict__ starts,
-                                                     const int32_t* __restrict__ adapter, int nreq,
-                                                     int m, int na, int TT, int min_len,
-                                                     int max_len, int piece, int* sm) {
-  LoraPiece r;
-  if (nreq == 1) {
-    const int b = lora_clamp(starts[0], m), e = lora_clamp(starts[1], m);
-    if (piece < lora_pieces(starts, 0, m, TT, min_len, max_len)) {
-      r.t0 = b + piece * TT;
-      r.cnt = min(TT, e - r.t0);
-      r.a = adapter[0];
-    }
-  } else {
-    int* found = sm + NT / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (nreq + NT - 1) / NT;
-    const int q0 = min(nreq, tid * per), q1 = min(nreq, q0 + per);
-    int own = 0;
-    for (int q = q0; q < q1; ++q) own += lora_pieces(starts, q, m, TT, min_len, max_len);
-    int inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) sm[warp] = inc;
-    if (tid == 0) found[1] = 0;
-    __syncthreads();
-    int before = inc - own;
-    for (int w = 0; w < warp; ++w) before += sm[w];
-    if (piece >= before && piece < before + own) {  // at most one thread
-      int left = piece - before, q = q0;
-      for (; q < q1; ++q) {
-        const int p = lora_pieces(starts, q, m, TT, min_len, max_len);
-        if (left < p) break;
-        left -= p;
-      }
-      const int t0 = lora_clamp(starts[q], m) + left * TT;
-      found[0] = t0;
-      found[1] = min(TT, lora_clamp(starts[q + 1], m) - t0);
-      found[2] = adapter[q];
-    }
-    __syncthreads();
-    r.t0 = found[0];
-    r.cnt = found[1];
-    r.a = r.cnt > 0 ? found[2] : -1;
-    __syncthreads();  // sm may be reused
-  }
-  if (r.a < 0 || r.a >= na) r.a = -1;
-  return r;
-}
-
 // ---- clusters ----------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -328,26 +271,8 @@ __device__ __forceinline__ void lora_copy_row(const T* y, T* o, int j0, int j1, 
         y != nullptr ? reinterpret_cast<const unsigned short*>(y)[j] : (unsigned short)0;
 }
 
-// The rows of a request without an adapter: out = Y (0 without Y) unless they are
-// the same, V = 0.  CTA `rank` of `nctas` takes its share of the columns, warp by warp a
-// row; `vec`: rows of Y and out start on 16-byte boundaries.
-template <typename T>
-__device__ __forceinline__ void lora_copy_piece(const LoraArgs& a, const LoraPiece& pc, int rank,
-                                                int nctas, int nthreads, int vec) {
-  if (a.out != nullptr && a.Y != a.out) {
-    const int per = ((a.N + nctas - 1) / nctas + 7) / 8 * 8;
-    const int j0 = min(a.N, rank * per), j1 = min(a.N, j0 + per);
-    for (int i = threadIdx.x / 32; i < pc.cnt; i += nthreads / 32) {
-      const int64_t row = pc.t0 + i;
-      lora_copy_row<T>(a.Y != nullptr ? (const T*)a.Y + row * a.ldy : nullptr,
-                       (T*)a.out + row * a.ldo, j0, j1, vec);
-    }
-  }
-  if (a.V != nullptr && rank == 0)
-    for (int e = threadIdx.x; e < pc.cnt * a.r; e += nthreads) a.V[(int64_t)pc.t0 * a.r + e] = 0.f;
-}
-
-// The same over the whole batch, for a launch whose pieces have adapters only: part
+// Rows without an adapter: out = Y (0 without Y) unless they are the same, V = 0, over
+// the whole batch, for a launch whose pieces have adapters only: part
 // `part` of `nparts` takes every nparts-th row of every such request; `nthreads` (a
 // multiple of 32) threads of the CTA call it, thread `tid` of them.
 template <typename T>

@@ -35,7 +35,8 @@ std::atomic<uint32_t> g_wait_limit{tc::kSpinLimit};
 }  // namespace
 
 cudaError_t smem_optin(const void* func, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;  // the default limit needs no opt-in
+  // the default limit (48 KB with the kernel's static shared memory) needs no opt-in
+  if (bytes <= 46 * 1024) return cudaSuccess;
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
