@@ -273,53 +273,53 @@ def _invalid(where: str, detail: str):
     raise GptqError(GPTQ_ERR_INVALID_ARG, where, detail)
 
 
-class _on_device:
-    """Makes the device of the first tensor current for a call (the library
-    launches on the current device) and checks that all tensors are on it; the
-    stream is the given one or that device's current stream."""
+# The operators below check every tensor's type, shape, strides and device in Python, since
+# the C ABI sees addresses only.  For a single token these checks cost as much as the
+# kernel, so they are written for few attribute reads.
 
-    __slots__ = ("dev", "prev", "stream")
 
-    def __init__(self, where, stream, first, *rest):
-        if not first.is_cuda:
-            _invalid(where, "tensor not on a CUDA device")
-        dev = first.get_device()
-        for t in rest:
-            if t is not None and t.get_device() != dev:
-                _invalid(where, "tensors on different devices")
-        self.dev = dev
-        if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(dev)
-        else:
-            if stream.device.index != dev:
-                _invalid(where, "stream of another device")
-            self.stream = stream.cuda_stream
+def _device(where, first, *rest):
+    """The CUDA device that all tensors share (None entries are left out)."""
+    dev = first.get_device()
+    if dev < 0:
+        _invalid(where, "tensor not on a CUDA device")
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            _invalid(where, "tensors on different devices")
+    return dev
 
-    def __enter__(self):
-        self.prev = torch._C._cuda_getDevice()
-        if self.prev != self.dev:
-            torch._C._cuda_setDevice(self.dev)
-        return self.stream
 
-    def __exit__(self, *exc):
-        if self.prev != self.dev:
-            torch._C._cuda_setDevice(self.prev)
-        return False
+def _call(where, dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current (the library launches on the current device),
+    on the given stream or that device's current one."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            _invalid(where, "stream of another device")
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != GPTQ_OK:
+        raise GptqError(st, where)
 
 
 def _rows(where, name, t, rows, cols, dtype):
     """A (rows, cols) matrix of dtype with unit column stride; its leading dimension."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.dtype != dtype:
+    if t.dtype is not dtype or t.shape != (rows, cols):
         _invalid(where, f"{name}: {tuple(t.shape)} {t.dtype}, want ({rows}, {cols}) {dtype}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, cs = t.stride()
+    if cs != 1 and cols > 1:
         _invalid(where, f"{name}: unit column stride")
-    ld = t.stride(0)
     return ld if rows > 1 and cols > 0 else max(ld, cols, 1)
 
 
 def _whole(where, name, t, shape, dtype):
     """A contiguous tensor of the given shape and dtype; its address."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         _invalid(where, f"{name}: {tuple(t.shape)} {t.dtype}, want contiguous {shape} {dtype}")
     return t.data_ptr()
 
@@ -327,34 +327,36 @@ def _whole(where, name, t, shape, dtype):
 def gemm_dgrad(dY, qweight, scales, zeros, g_idx, bits, group_size, k, dX, stream=None):
     """dX = dY W_hat from the packed weights (gptq_gemm_dgrad)."""
     w = "gptq_gemm_dgrad"
+    if dY.dim() != 2 or scales.dim() != 2:
+        _invalid(w, "dY (m, n), scales (n, ngroups)")
     m, n = dY.shape
     ng = scales.shape[1]
-    dt = dtype_code(dY.dtype)
+    dtype = dY.dtype
+    dt = dtype_code(dtype)
     if bits not in (2, 3, 4, 8):
         raise GptqError(GPTQ_ERR_UNSUPPORTED, w, f"bits {bits}")
-    ldy, ldx = _rows(w, "dY", dY, m, n, dY.dtype), _rows(w, "dX", dX, m, k, dY.dtype)
+    ldy, ldx = _rows(w, "dY", dY, m, n, dtype), _rows(w, "dX", dX, m, k, dtype)
     qw = _whole(w, "qweight", qweight, (n, k * bits // 32), torch.int32)
     sc = _whole(w, "scales", scales, (n, ng), torch.float32)
     ze = _whole(w, "zeros", zeros, (n, ng), torch.int32)
     gi = _whole(w, "g_idx", g_idx, (k,), torch.int32) if g_idx is not None else None
-    with _on_device(w, stream, dY, qweight, scales, zeros, g_idx, dX) as s:
-        _check(load().gptq_gemm_dgrad(dY.data_ptr(), dt, m, n, ldy, qw, sc, ze, gi, k, bits,
-                                      group_size, ng, dX.data_ptr(), ldx, s), w)
+    dev = _device(w, dY, qweight, scales, zeros, g_idx, dX)
+    _call(w, dev, stream, load().gptq_gemm_dgrad, dY.data_ptr(), dt, m, n, ldy, qw, sc, ze, gi, k,
+          bits, group_size, ng, dX.data_ptr(), ldx)
 
 
 def _adapters(w, A, B, scaling, starts, adapter, dtype):
-    """Checks the adapters and the requests; (na, rank, k, n, nreq)."""
-    if A.dim() != 3 or B.dim() != 3:
-        _invalid(w, "A (na, rank, k), B (na, n, rank)")
+    """Checks the adapters and the requests; sizes (na, rank, k, n, nreq) and addresses."""
+    if A.dim() != 3 or B.dim() != 3 or adapter.dim() != 1:
+        _invalid(w, "A (na, rank, k), B (na, n, rank), adapter (requests,)")
     na, r, k = A.shape
     n = B.shape[1]
-    _whole(w, "A", A, (na, r, k), dtype)
-    _whole(w, "B", B, (na, n, r), dtype)
-    _whole(w, "scaling", scaling, (na,), torch.float32)
-    nreq = adapter.shape[0] if adapter.dim() == 1 else -1
-    _whole(w, "adapter", adapter, (nreq,), torch.int32)
-    _whole(w, "starts", starts, (nreq + 1,), torch.int32)
-    return na, r, k, n, nreq
+    nreq = len(adapter)
+    return na, r, k, n, nreq, (
+        _whole(w, "A", A, (na, r, k), dtype), _whole(w, "B", B, (na, n, r), dtype),
+        _whole(w, "scaling", scaling, (na,), torch.float32),
+        _whole(w, "starts", starts, (nreq + 1,), torch.int32),
+        _whole(w, "adapter", adapter, (nreq,), torch.int32))
 
 
 def lora_add(Y, X, A, B, scaling, starts, adapter, out, V=None, stream=None):
@@ -362,17 +364,20 @@ def lora_add(Y, X, A, B, scaling, starts, adapter, out, V=None, stream=None):
     w = "gptq_lora_add"
     dtype = X.dtype
     dt = dtype_code(dtype)
-    na, r, k, n, nreq = _adapters(w, A, B, scaling, starts, adapter, dtype)
-    m = X.shape[0]
+    na, r, k, n, nreq, (pa, pb, ps, pst, pad) = _adapters(w, A, B, scaling, starts, adapter, dtype)
+    m = len(X)
     ldx, ldo = _rows(w, "X", X, m, k, dtype), _rows(w, "out", out, m, n, dtype)
-    yp, ldy = None, 0
-    if Y is not None:
-        yp, ldy = Y.data_ptr(), _rows(w, "Y", Y, m, n, dtype)
-    vp = _whole(w, "V", V, (m, r), torch.float32) if V is not None else None
-    with _on_device(w, stream, X, Y, A, B, scaling, starts, adapter, out, V) as s:
-        _check(load().gptq_lora_add(yp, ldy, X.data_ptr(), dt, m, k, ldx, A.data_ptr(),
-                                    B.data_ptr(), scaling.data_ptr(), na, r, starts.data_ptr(),
-                                    adapter.data_ptr(), nreq, n, out.data_ptr(), ldo, vp, s), w)
+    po = out.data_ptr()
+    if Y is None:
+        py, ldy = None, 0
+    elif Y is out:
+        py, ldy = po, ldo
+    else:
+        py, ldy = Y.data_ptr(), _rows(w, "Y", Y, m, n, dtype)
+    pv = _whole(w, "V", V, (m, r), torch.float32) if V is not None else None
+    dev = _device(w, X, Y, A, B, scaling, starts, adapter, out, V)
+    _call(w, dev, stream, load().gptq_lora_add, py, ldy, X.data_ptr(), dt, m, k, ldx, pa, pb, ps, na,
+          r, pst, pad, nreq, n, po, ldo, pv)
 
 
 def lora_backward(dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB, ws,
@@ -381,46 +386,47 @@ def lora_backward(dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, d
     w = "gptq_lora_backward"
     dtype = dY.dtype
     dt = dtype_code(dtype)
-    na, r, k, n, nreq = _adapters(w, A, B, scaling, starts, adapter, dtype)
-    m = dY.shape[0]
+    na, r, k, n, nreq, (pa, pb, ps, pst, pad) = _adapters(w, A, B, scaling, starts, adapter, dtype)
+    m = len(dY)
     ldy = _rows(w, "dY", dY, m, n, dtype)
     ldx = _rows(w, "X", X, m, k, dtype if x_scales is None else torch.int8)
     xs = None
     if x_scales is not None:
         xs = _whole(w, "x_scales", x_scales, (m, (k + 127) // 128), torch.float32)
-    vp = _whole(w, "V", V, (m, r), torch.float32)
-    dxp, ldd, op, ldo = None, 0, None, 0
+    pv = _whole(w, "V", V, (m, r), torch.float32)
+    pdx, ldd, po, ldo = None, 0, None, 0
     if out is not None:
-        op, ldo = out.data_ptr(), _rows(w, "out", out, m, k, dtype)
-        if dX is not None:
-            dxp, ldd = dX.data_ptr(), _rows(w, "dX", dX, m, k, dtype)
+        po, ldo = out.data_ptr(), _rows(w, "out", out, m, k, dtype)
+        if dX is out:
+            pdx, ldd = po, ldo
+        elif dX is not None:
+            pdx, ldd = dX.data_ptr(), _rows(w, "dX", dX, m, k, dtype)
     da, db = _whole(w, "dA", dA, (na, r, k), dtype), _whole(w, "dB", dB, (na, n, r), dtype)
-    nws = ws.numel() * ws.element_size()
-    with _on_device(w, stream, dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB,
-                    ws) as s:
-        _check(load().gptq_lora_backward(dY.data_ptr(), dt, m, n, ldy, X.data_ptr(), ldx, xs, k,
-                                         vp, A.data_ptr(), B.data_ptr(), scaling.data_ptr(), na, r,
-                                         starts.data_ptr(), adapter.data_ptr(), nreq, dxp, ldd, op,
-                                         ldo, da, db, ws.data_ptr(), nws, s), w)
+    dev = _device(w, dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB, ws)
+    _call(w, dev, stream, load().gptq_lora_backward, dY.data_ptr(), dt, m, n, ldy, X.data_ptr(), ldx,
+          xs, k, pv, pa, pb, ps, na, r, pst, pad, nreq, pdx, ldd, po, ldo, da, db, ws.data_ptr(),
+          ws.nbytes)
 
 
 def act_checkpoint(X, codes, scales, stream=None):
     """8-bit codes and block scales of X (gptq_act_checkpoint)."""
     w = "gptq_act_checkpoint"
     m, k = X.shape
-    ldx, ldc = _rows(w, "X", X, m, k, X.dtype), _rows(w, "codes", codes, m, k, torch.int8)
+    dtype = X.dtype
+    dt = dtype_code(dtype)
+    ldx, ldc = _rows(w, "X", X, m, k, dtype), _rows(w, "codes", codes, m, k, torch.int8)
     sp = _whole(w, "scales", scales, (m, (k + 127) // 128), torch.float32)
-    with _on_device(w, stream, X, codes, scales) as s:
-        _check(load().gptq_act_checkpoint(X.data_ptr(), dtype_code(X.dtype), m, k, ldx,
-                                          codes.data_ptr(), ldc, sp, s), w)
+    _call(w, _device(w, X, codes, scales), stream, load().gptq_act_checkpoint, X.data_ptr(), dt, m, k,
+          ldx, codes.data_ptr(), ldc, sp)
 
 
 def act_restore(codes, scales, out, stream=None):
     """The activations of a checkpoint (gptq_act_restore)."""
     w = "gptq_act_restore"
     m, k = codes.shape
-    ldc, ldo = _rows(w, "codes", codes, m, k, torch.int8), _rows(w, "out", out, m, k, out.dtype)
+    dtype = out.dtype
+    dt = dtype_code(dtype)
+    ldc, ldo = _rows(w, "codes", codes, m, k, torch.int8), _rows(w, "out", out, m, k, dtype)
     sp = _whole(w, "scales", scales, (m, (k + 127) // 128), torch.float32)
-    with _on_device(w, stream, codes, scales, out) as s:
-        _check(load().gptq_act_restore(codes.data_ptr(), ldc, sp, m, k, dtype_code(out.dtype),
-                                       out.data_ptr(), ldo, s), w)
+    _call(w, _device(w, codes, scales, out), stream, load().gptq_act_restore, codes.data_ptr(), ldc,
+          sp, m, k, dt, out.data_ptr(), ldo)

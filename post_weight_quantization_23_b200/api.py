@@ -196,13 +196,13 @@ def quant_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
     return out
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(dtype, device, stream, *shape):
     """A new tensor that belongs to the stream the call runs on (the caching
     allocator reuses its memory in that stream's order)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def quant_matmul_dgrad(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
@@ -213,7 +213,7 @@ def quant_matmul_dgrad(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     device, the weights as for quant_matmul.  Returns dX (m, k) in dY's dtype
     (``out`` if given)."""
     if out is None:
-        out = _empty((dY.shape[0], k), dY.dtype, dY.device, stream)
+        out = _empty(dY.dtype, dY.device, stream, len(dY), k)
     _lib.gemm_dgrad(dY, qweight, scales, zeros, g_idx, bits, group_size, k, out, stream)
     return out
 
@@ -258,12 +258,12 @@ def lora_backward(dY: torch.Tensor, X: torch.Tensor, V: torch.Tensor, A: torch.T
     if out is None:
         out = dX
     if dA is None:
-        dA = _empty(A.shape, A.dtype, A.device, stream)
+        dA = _empty(A.dtype, A.device, stream, *A.shape)
     if dB is None:
-        dB = _empty(B.shape, B.dtype, B.device, stream)
+        dB = _empty(B.dtype, B.device, stream, *B.shape)
     if ws is None:
-        nbytes = _lib.workspace_size(_lib.OP_LORA_BACKWARD, A.shape[1], 0, dY.shape[0], None)
-        ws = _empty((max(nbytes, 1),), torch.uint8, dY.device, stream)
+        nbytes = _lib.workspace_size(_lib.OP_LORA_BACKWARD, A.shape[1], 0, len(dY), None)
+        ws = _empty(torch.uint8, dY.device, stream, max(nbytes, 1))
     _lib.lora_backward(dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB, ws,
                        stream)
     return out, dA, dB
@@ -276,9 +276,9 @@ def act_checkpoint(X: torch.Tensor, codes: torch.Tensor | None = None,
     one per row and block of 128 columns.  Returns (codes, scales)."""
     m, k = X.shape
     if codes is None:
-        codes = _empty((m, k), torch.int8, X.device, stream)
+        codes = _empty(torch.int8, X.device, stream, m, k)
     if scales is None:
-        scales = _empty((m, (k + 127) // 128), torch.float32, X.device, stream)
+        scales = _empty(torch.float32, X.device, stream, m, (k + 127) // 128)
     _lib.act_checkpoint(X, codes, scales, stream)
     return codes, scales
 
@@ -288,7 +288,7 @@ def act_restore(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float16,
     """The activations that act_checkpoint kept, codes * scales (gptq_act_restore),
     in ``dtype`` (or into ``out``)."""
     if out is None:
-        out = _empty(codes.shape, dtype, codes.device, stream)
+        out = _empty(dtype, codes.device, stream, *codes.shape)
     _lib.act_restore(codes, scales, out, stream)
     return out
 
