@@ -125,7 +125,9 @@ struct DtShape {
   static constexpr int STAGE = A + B + P;
   static constexpr int S = MT == 2 ? 3 : 4;     // stages, and dequantizing groups
   static constexpr int THREADS = 64 + 32 * DT_GROUP * S;
-  static constexpr size_t SMEM = (size_t)S * STAGE + 256;
+  // the grids of a group's stage: 64 rows x up to one group per 32 columns
+  static constexpr int GRID = MT * 4 * DT_K * 6;
+  static constexpr size_t SMEM = (size_t)S * (STAGE + GRID) + 256;
   static_assert(SMEM <= 232448 && STAGE % 1024 == 0, "shared memory of a CTA");
 };
 
@@ -145,6 +147,8 @@ template <> struct DtType<false> {
   using T2 = __half2;
   static constexpr uint32_t MAGIC = 0x64006400u;  // 1024 in both halves: ulp 1 on [1024, 2048)
   static constexpr float BASE = 1024.f;
+  __device__ static T one(float v) { return __float2half_rn(v); }
+  __device__ static T2 both(T v) { return __half2half2(v); }
   __device__ static T2 pair(float v) { return __float2half2_rn(v); }
   __device__ static float back(T2 v) { return __low2float(v); }
 };
@@ -153,6 +157,8 @@ template <> struct DtType<true> {
   using T2 = __nv_bfloat162;
   static constexpr uint32_t MAGIC = 0x43004300u;  // 128 in both halves: ulp 1 on [128, 256)
   static constexpr float BASE = 128.f;
+  __device__ static T one(float v) { return __float2bfloat16_rn(v); }
+  __device__ static T2 both(T v) { return __bfloat162bfloat162(v); }
   __device__ static T2 pair(float v) { return __float2bfloat162_rn(v); }
   __device__ static float back(T2 v) { return __low2float(v); }
 };
@@ -166,7 +172,8 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
   using Sh = DtShape<MT>;
   constexpr int S = Sh::S;
   extern __shared__ __align__(1024) uint8_t dt_smem[];
-  uint64_t* bars = (uint64_t*)(dt_smem + S * Sh::STAGE);
+  uint8_t* grids = dt_smem + S * Sh::STAGE;
+  uint64_t* bars = (uint64_t*)(grids + S * Sh::GRID);
   uint64_t* full = bars;            // [S] packed words and dY landed
   uint64_t* ready = bars + S;       // [S] the weights are written
   uint64_t* empty = bars + 2 * S;   // [S] the stage's MMAs are done
@@ -192,9 +199,14 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
     tc::prefetch_tensormap(&ymap);
     tc::prefetch_tensormap(&pmap);
   }
-  pdl_wait();
+  // Only dY comes from the kernel before, and only dX may still be read by it: the copies
+  // of dY and the stores wait for it, the grids are requested at once (the packed weights
+  // must not be written by a kernel that lets this one start early).
   pdl_trigger();
-  if (warp == 1) tc::tmem_alloc(tmem_slot, MT * 256);
+  if (warp == 1) {
+    pdl_wait();  // its CTAs have given their TMEM back
+    tc::tmem_alloc(tmem_slot, MT * 256);
+  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -203,6 +215,7 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t bytes = Sh::P + (uint32_t)a.N * DT_K * 2;
+      pdl_wait();
       for (int it = 0; it < ns; ++it) {
         const int s = it % S;
         if (it >= S && !tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, a.spin))
@@ -223,7 +236,7 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
       int s = 0;
       uint32_t ph = 0;
       for (int it = 0; it < ns; ++it) {
-        if (!tc::mbar_wait(&full[s], ph, abort_flag, a.spin)) break;
+        // the dequantizing warps waited for the copies before they arrived
         if (!tc::mbar_wait(&ready[s], ph, abort_flag, a.spin)) break;
         tc::tc_fence_after();
         const uint64_t w = tc::desc_add(dw, (uint32_t)s * Sh::STAGE);
@@ -244,32 +257,56 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
     // quads (32 columns) MT gw .. of rows lane and lane + 32; neighbouring lanes are
     // neighbouring rows
     constexpr int R = 2 * MT;
-    int g[MT];
-#pragma unroll
-    for (int q = 0; q < MT; ++q) g[q] = min(c0 + 32 * (MT * gw + q), a.k - 1) / a.G;
-    float sc[R], ze[R];
+    // The grids: thread = (row, every second group of the tile) of the group's next stage,
+    // requested a stage of the group ahead and handed round through shared memory.  (Each
+    // thread fetching those of its own runs cost four times the scattered loads: 32 rows
+    // are 32 lines, and the L1 looks up one a cycle.)
+    const int gt = gw * 32 + lane, grow = gt % DT_K, ghalf = gt / DT_K;
+    const int g0 = c0 / a.G, ng = (min(c0 + MT * 128, a.k) - 1) / a.G - g0 + 1;
+    float* gsc = (float*)(grids + grp * Sh::GRID);                              // [4 MT][64]
+    typename Ty::T* gze = (typename Ty::T*)(grids + grp * Sh::GRID + MT * 4 * DT_K * 4);
+    float fs[R];
+    int fz[R];
     auto fetch = [&](int it) {
+      const int j = it * DT_K + grow;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int j = it * DT_K + lane + 32 * (r & 1);
-        const bool ok = it < ns && j < a.n;
-        const int64_t at = (int64_t)j * a.ngroups + g[r / 2];
-        sc[r] = ok ? __ldg(a.scales + at) : 0.f;
-        ze[r] = ok ? (float)__ldg(a.zeros + at) : 0.f;
+      for (int i = 0; i < R; ++i) {
+        const bool ok = ghalf + 2 * i < ng && it < ns && j < a.n;
+        const int64_t at = (int64_t)j * a.ngroups + g0 + ghalf + 2 * i;
+        fs[i] = ok ? __ldg(a.scales + at) : 0.f;
+        fz[i] = ok ? __ldg(a.zeros + at) : 0;
       }
     };
+    int gq[MT];  // the group slot of each quad
+#pragma unroll
+    for (int q = 0; q < MT; ++q) gq[q] = min(c0 + 32 * (MT * gw + q), a.k - 1) / a.G - g0;
     fetch(grp);
+    bool gave_up = false;
     for (int it = grp; it < ns; it += S) {
       const int s = it % S;
+      // the last stage's grids are read; a give-up ends the loop of the whole group
+      if (tc::named_bar_any(1 + grp, 32 * DT_GROUP, gave_up)) break;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (ghalf + 2 * i < ng) {
+          gsc[(ghalf + 2 * i) * DT_K + grow] = fs[i];
+          gze[(ghalf + 2 * i) * DT_K + grow] = Ty::one(Ty::BASE + (float)fz[i]);  // exact, |zero| <= 127
+        }
+      tc::named_bar_sync(1 + grp, 32 * DT_GROUP);
+      fetch(it + S);
       T2 hi[R], lo[R], zz[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        hi[r] = Ty::pair(sc[r]);
-        lo[r] = Ty::pair(sc[r] - Ty::back(hi[r]));
-        zz[r] = Ty::pair(Ty::BASE + ze[r]);  // exact for |zero| <= 127
+        const int at = gq[r / 2] * DT_K + lane + 32 * (r & 1);
+        const float sc = gsc[at];
+        hi[r] = Ty::pair(sc);
+        lo[r] = Ty::pair(sc - Ty::back(hi[r]));
+        zz[r] = Ty::both(gze[at]);
       }
-      fetch(it + S);
-      if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin)) break;
+      if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin)) {
+        gave_up = true;
+        continue;
+      }
       uint8_t* sb = stage(it);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -304,6 +341,7 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
     // epilogue: this warp's lane quarter of the 128-column tiles, its share of the tokens
     const bool ok = tc::mbar_wait_warp(done, 0, abort_flag, a.spin) && !*abort_flag;
     tc::tc_fence_after();
+    pdl_wait();
     const int quarter = warp & 3, nch = (a.N + 31) / 32;  // 32-token chunks of a tile
     for (int x = grp; x < MT * nch; x += S) {
       const int mt = x / nch, q = x % nch * 32;
@@ -342,16 +380,19 @@ bool dgrad_tc_supported(const void* dY, int64_t lddy, const int32_t* qw, int bit
 }
 
 // Columns (MT * 128) and tokens (N, a multiple of 16) of a tile: the pair whose waves
-// over the SMs cost least, a stage of a wave counted as its MMAs (2 MT N cycles) or its
-// dequantization, whichever is longer.
+// over the SMs cost least.  A stage costs its MMAs (2 MT N cycles) or, more often, its
+// shared-memory traffic at 128 bytes a cycle: copies N 128 + MT 4096, weights MT (4096 +
+// 16384) read and written, operands MT (16384 + N 128) read by the MMAs.  Measured
+// (22016 x 4096, 4096 tokens): 2 x 128 columns with 240 tokens 659 us, 256 tokens 678,
+// 128 columns with 240 tokens 746.
 void launch_shape(int64_t m, int64_t k, int& MT, int& N) {
   const int sms = sm_count();
-  double best = 0;
+  int64_t best = 0;
   for (int mt = 1; mt <= 2; ++mt)
     for (int nn = 16; nn <= DT_NMAX; nn += 16) {
       const int64_t tiles = cdiv(k, mt * 128) * cdiv(m, nn);
-      const double cost = (double)cdiv(tiles, sms) * std::max(2.0 * mt * nn, 200.0 * mt + 200.0);
-      if (best == 0 || cost < best * 0.999) best = cost, MT = mt, N = nn;
+      const int64_t cost = cdiv(tiles, sms) * std::max(2 * mt * nn, nn * (1 + mt) + 320 * mt);
+      if (best == 0 || cost < best) best = cost, MT = mt, N = nn;
     }
 }
 
