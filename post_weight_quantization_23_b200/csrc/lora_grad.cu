@@ -11,7 +11,9 @@
 // shared memory in a fixed order), D[128 x RP] fp32 in TMEM, tokens as the MMA's K.
 // Both operands are MN-major: rows of S as TMA brings them, and rows of W.
 //   W is split into two bf16 parts, hi + lo (16 significant bits; bf16 for its range:
-//     gradients are small, f16 would lose them among its subnormals).
+//     gradients are small, f16 would lose them among its subnormals), side by side as one
+//     operand of 2 RP columns: S is read from shared memory, whose bandwidth sets the
+//     pace, once for both, and the two halves of D are added at the end.
 //   S in bf16 is used as it is.  S in f16 is split into two bf16 parts as well (exact but
 //     for f16's smallest subnormals), three products, lo x lo left out.
 //   S in 8-bit codes becomes bf16 exactly (|code| <= 127), and its scales, one per token
@@ -126,22 +128,26 @@ constexpr int GT_TABLE = 128;                // tiles looked up at a time
 constexpr int GT_LD = GT_C + 1;              // row stride of the staged sums (no bank conflicts)
 constexpr int GT_BARS = 384;                 // bytes of barriers and small words
 
-// A slot of the operand ring: S hi (and lo), W hi and lo.  Tiles to be converted (f16,
+// A slot of the operand ring: S hi (and lo), W hi | lo.  Tiles to be converted (f16,
 // codes) land in RAW bytes behind the slots.
 template <int RP, bool F16>
 struct GtShape {
-  static constexpr int W = (RP > 64 ? 2 : 1) * GT_ATOM;
   static constexpr int HI = 0, LO = 2 * GT_ATOM;
-  static constexpr int WHI = (F16 ? 4 : 2) * GT_ATOM, WLO = WHI + W;
-  static constexpr int STAGE = WLO + W;
+  static constexpr int W = (F16 ? 4 : 2) * GT_ATOM;  // 2 RP columns in atoms of 64
+  static constexpr int STAGE = W + (2 * RP + 63) / 64 * GT_ATOM;
   static constexpr int S = F16 ? (RP > 64 ? 2 : 3) : 4;
   // groups of operand warps: as many as slots, where their registers allow it
   static constexpr int NG = RP <= 64 ? S : 2;
   static constexpr int RAW = (RP > 64 ? 4 : F16 ? 6 : 8) * GT_ATOM;
   static constexpr int R_CODES = RAW / GT_ATOM, R_F16 = RAW / (2 * GT_ATOM);
+  // a bf16 S needs no raw ring: its place holds more slots, for fewer groups (their work
+  // is half of that on codes, the copies' latency is what is left to cover)
+  static constexpr int S_DIRECT = RP <= 64 ? 6 : 4, NG_DIRECT = RP <= 64 ? 3 : 2;
   static constexpr int THREADS = 64 + 128 * NG;
-  static_assert(S % NG == 0 && R_CODES % NG == 0 && (!F16 || R_F16 % NG == 0),
+  static_assert(S % NG == 0 && R_CODES % NG == 0 && (!F16 || R_F16 % NG == 0) &&
+                    S_DIRECT % NG_DIRECT == 0 && (F16 || NG_DIRECT <= NG),
                 "a slot belongs to one group");
+  static_assert(F16 || S_DIRECT * STAGE <= S * STAGE + RAW, "the slots of bf16 tiles fit");
   static constexpr int SUMS = RP * GT_LD * 4;
   static constexpr size_t SMEM =
       (size_t)S * STAGE + RAW + GT_BARS + GT_TABLE * sizeof(LoraPiece);
@@ -187,21 +193,21 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                  LoraGradArgs ga, LoraGradArgs gb, LoraGradCommon c, int blocks_a, int split) {
   using Sh = GtShape<RP, F16>;
   using T = typename LoraType<!F16>::T;
-  constexpr int S = Sh::S, NG = Sh::NG, GT_THREADS = Sh::THREADS;
+  constexpr int GT_THREADS = Sh::THREADS;
   extern __shared__ __align__(1024) uint8_t gt_smem[];
-  uint8_t* raws = gt_smem + S * Sh::STAGE;
+  uint8_t* raws = gt_smem + Sh::S * Sh::STAGE;
   uint64_t* bars = (uint64_t*)(raws + Sh::RAW);
   uint64_t* full = bars;            // [8] the tile landed (in a slot, or in the raw ring)
   uint64_t* rawfree = bars + 8;     // [8] the raw tile is converted
-  uint64_t* ready = bars + 16;      // [S] both operands are written
-  uint64_t* empty = ready + S;      // [S] the MMAs that read them are done
-  uint64_t* done = empty + S;
+  uint64_t* ready = bars + 16;      // [6] both operands are written
+  uint64_t* empty = ready + 6;      // [6] the MMAs that read them are done
+  uint64_t* done = empty + 6;
   uint32_t* tmem_slot = (uint32_t*)(done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;
   int* scan = (int*)(tmem_slot + 3);  // GT_THREADS / 32 + 1 ints
   LoraPiece* table = (LoraPiece*)(raws + Sh::RAW + GT_BARS);
-  static_assert((16 + 2 * S + 1) * 8 + 12 + 4 * (GT_THREADS / 32 + 1) <= GT_BARS, "fits");
+  static_assert((16 + 2 * 6 + 1) * 8 + 12 + 4 * (GT_THREADS / 32 + 1) <= GT_BARS, "fits");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int part = (int)blockIdx.x % split, blk = (int)blockIdx.x / split;
@@ -211,15 +217,16 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   const int col0 = (second ? blk - blocks_a : blk) * GT_C, ad = blockIdx.y;
   const bool codes = g.s_scales != nullptr;
   const bool convert = F16 || codes;
-  // slots that the copies go round
+  // slots of the operands, their groups of warps, slots that the copies go round
+  const int S = convert ? Sh::S : Sh::S_DIRECT, NG = convert ? Sh::NG : Sh::NG_DIRECT;
   const int R = codes ? Sh::R_CODES : F16 ? Sh::R_F16 : S;
-  constexpr int TM = RP < 32 ? 32 : RP;
+  constexpr int TM = 2 * RP;  // TMEM columns
   if (threadIdx.x == 0) {
     for (int s = 0; s < 8; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&rawfree[s], 4);
     }
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < 6; ++s) {
       tc::mbar_init(&ready[s], 4);
       tc::mbar_init(&empty[s], 1);
     }
@@ -263,7 +270,9 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
       }
     } else if (warp == 1) {
       if (tc::elect_one()) {
-        const uint32_t id = tc::instr_desc(1, GT_C, RP, 1, 1);  // bf16, both MN-major
+        // bf16, both MN-major; S hi times W hi | lo, S lo (f16) times W hi
+        const uint32_t id = tc::instr_desc(1, GT_C, 2 * RP, 1, 1);
+        const uint32_t id_lo = tc::instr_desc(1, GT_C, RP, 1, 1);
         const uint64_t d0 = tc::smem_desc_sw128(tc::smem_u32(gt_smem), GT_ATOM, 1024);
         const bool split_s = F16 && !codes;
         int s = base % S;
@@ -273,15 +282,12 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
           if (!tc::mbar_wait(&ready[s], ph, abort_flag, c.spin)) break;
           tc::tc_fence_after();
           const uint64_t d = tc::desc_add(d0, (uint32_t)s * Sh::STAGE);
-          auto mma = [&](int x, int w, int kk, uint32_t acc) {
-            tc::mma_f16_ss(tmem, tc::desc_add(d, x + kk * 2048), tc::desc_add(d, w + kk * 2048), id,
-                           acc);
-          };
 #pragma unroll
           for (int kk = 0; kk < GT_T / 16; ++kk) {
-            mma(Sh::HI, Sh::WLO, kk, kk > 0 ? 1u : (uint32_t)(base + i > 0));
-            if (split_s) mma(Sh::LO, Sh::WHI, kk, 1u);
-            mma(Sh::HI, Sh::WHI, kk, 1u);
+            const uint64_t w = tc::desc_add(d, Sh::W + kk * 2048);
+            tc::mma_f16_ss(tmem, tc::desc_add(d, Sh::HI + kk * 2048), w, id,
+                           kk > 0 ? 1u : (uint32_t)(base + i > 0));
+            if (split_s) tc::mma_f16_ss(tmem, tc::desc_add(d, Sh::LO + kk * 2048), w, id_lo, 1u);
           }
           tc::mma_commit(&empty[s]);
           if (++s == S) s = 0, ph ^= 1u;
@@ -291,24 +297,42 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
       // ---- operands: group `grp` of four warps takes every NG-th tile ----
       const int grp = (warp - 2) / 4, gt = (warp - 2) % 4 * 32 + lane;
       constexpr int NCH = RP / 8;                 // 8-value chunks of a row of W
-      constexpr int TASKS = GT_T * NCH / 128;     // chunks per thread
+      constexpr int TASKS = GT_T * NCH / 128;     // chunks per thread: tokens wt + k WT
+      constexpr int WT = 128 / NCH;               // a multiple of 8 where TASKS > 1
       const int nb = (g.C + 127) / 128;
+      const int wt = gt / NCH, wc = gt % NCH, wl = NCH + wc;
+      const bool wcol = 8 * wc < c.r;
+      // places in shared memory (rows are 128 bytes; WT and 16 rows further on the swizzle
+      // is the same): W hi and lo of task k at + k WT 128, codes of task k at + k 2048
+      const int o_hi = Sh::W + (wc / 8) * GT_ATOM + wt * 128 + (((wc % 8) ^ (wt & 7)) << 4);
+      const int o_lo = Sh::W + (wl / 8) * GT_ATOM + wt * 128 + (((wl % 8) ^ (wt & 7)) << 4);
+      const int ct = gt / 8, cj = gt % 8, odd = cj / 4;
+      // eight lanes write a row of both atoms, whose banks are the same: those of the second
+      // atom write their odd chunk first
+      const int o_c0 = Sh::HI + odd * GT_ATOM + ct * 128 + (((2 * (cj % 4) + odd) ^ (ct & 7)) << 4);
+      const int o_c1 = o_c0 ^ 16;
       float4 w[TASKS][2];
       float sc[TASKS];
       auto fetch = [&](int i) {
         const LoraPiece p = table[i];
+        const float* src = g.W + (int64_t)(p.t0 + wt) * c.r + 8 * wc;
+        const float* ssc = codes ? g.s_scales + (int64_t)(p.t0 + wt) * nb + col0 / 128 : nullptr;
+        const int left = p.cnt - wt;
 #pragma unroll
         for (int k = 0; k < TASKS; ++k) {
-          const int e = gt + 128 * k, t = e / NCH, ch = e % NCH;
-          const bool have = t < p.cnt && 8 * ch < c.r;
-          const float* src = g.W + (int64_t)(p.t0 + t) * c.r + 8 * ch;
+          const bool have = wcol && k * WT < left;
           const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
           w[k][0] = have ? __ldg(reinterpret_cast<const float4*>(src)) : z;
           w[k][1] = have ? __ldg(reinterpret_cast<const float4*>(src) + 1) : z;
-          sc[k] = codes && have ? __ldg(g.s_scales + (int64_t)(p.t0 + t) * nb + col0 / 128) : 1.f;
+          sc[k] = 1.f;
+          if (codes) {
+            if (have) sc[k] = __ldg(ssc);
+            ssc += WT * nb;
+          }
+          src += WT * c.r;
         }
       };
-      int i = (grp - base % NG + NG) % NG;
+      int i = grp < NG ? (grp - base % NG + NG) % NG : np;
       if (i < np) fetch(i);
       for (; i < np; i += NG) {
         const int it = base + i, s = it % S, q = it % R;
@@ -320,31 +344,31 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
         uint8_t* sb = stage(s);
 #pragma unroll
         for (int k = 0; k < TASKS; ++k) {
-          const int e = gt + 128 * k, t = e / NCH, ch = e % NCH;
-          const float f = sc[k];
           uint4 hi, lo;
-          lora_split_bf16(w[k][0].x * f, w[k][0].y * f, hi.x, lo.x);
-          lora_split_bf16(w[k][0].z * f, w[k][0].w * f, hi.y, lo.y);
-          lora_split_bf16(w[k][1].x * f, w[k][1].y * f, hi.z, lo.z);
-          lora_split_bf16(w[k][1].z * f, w[k][1].w * f, hi.w, lo.w);
-          const int o = (ch / 8) * GT_ATOM + t * 128 + (((ch % 8) ^ (t & 7)) << 4);
-          *reinterpret_cast<uint4*>(sb + Sh::WHI + o) = hi;
-          *reinterpret_cast<uint4*>(sb + Sh::WLO + o) = lo;
+          if (codes) {
+            const float f = sc[k];
+            w[k][0].x *= f, w[k][0].y *= f, w[k][0].z *= f, w[k][0].w *= f;
+            w[k][1].x *= f, w[k][1].y *= f, w[k][1].z *= f, w[k][1].w *= f;
+          }
+          lora_split_bf16(w[k][0].x, w[k][0].y, hi.x, lo.x);
+          lora_split_bf16(w[k][0].z, w[k][0].w, hi.y, lo.y);
+          lora_split_bf16(w[k][1].x, w[k][1].y, hi.z, lo.z);
+          lora_split_bf16(w[k][1].z, w[k][1].w, hi.w, lo.w);
+          *reinterpret_cast<uint4*>(sb + o_hi + k * (WT * 128)) = hi;
+          *reinterpret_cast<uint4*>(sb + o_lo + k * (WT * 128)) = lo;
         }
         if (i + NG < np) fetch(i + NG);
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
         if (codes) {
+          const uint8_t* raw = raws + q * GT_ATOM + 16 * gt;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // 16 codes each
-            const int e = gt + 128 * k, t = e / 8, j = e % 8;
-            const uint4 u =
-                *reinterpret_cast<const uint4*>(raws + q * GT_ATOM + t * 128 + 16 * j);
-            const bool have = t < cnt;
-            uint8_t* row = sb + Sh::HI + (j / 4) * GT_ATOM + t * 128;
-            const int ch = 2 * (j % 4);
-            *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = have ? gt_codes(u.x, u.y) : z;
-            *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) =
-                have ? gt_codes(u.z, u.w) : z;
+            const uint4 u = *reinterpret_cast<const uint4*>(raw + 2048 * k);
+            uint4 x = gt_codes(odd ? u.z : u.x, odd ? u.w : u.y);
+            uint4 y = gt_codes(odd ? u.x : u.z, odd ? u.y : u.w);
+            if (ct + 16 * k >= cnt) x = y = z;
+            *reinterpret_cast<uint4*>(sb + o_c0 + 2048 * k) = x;
+            *reinterpret_cast<uint4*>(sb + o_c1 + 2048 * k) = y;
           }
         } else if (F16) {
 #pragma unroll
@@ -388,19 +412,18 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
   float* sums = (float*)gt_smem;  // [RP][GT_LD]
   if (warp >= 2 && warp < 10) {
     const int quarter = warp & 3, hf = (warp - 2) / 4, col = quarter * 32 + lane;
-    constexpr int HC = RP / 2, CW = HC < 32 ? HC : 32;
+    constexpr int HC = RP / 2, CW = HC < 16 ? HC : 16;
 #pragma unroll
     for (int q = 0; q < HC; q += CW) {
-      float v[CW];
+      float v[CW], l[CW];
       const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(hf * HC + q);
-      if (CW == 8) tc::tmem_ld_32x32b_x8(ta, v);
-      else if (CW == 16) tc::tmem_ld_32x32b_x16(ta, v);
-      else tc::tmem_ld_32x32b_x32(ta, v);
+      if (CW == 8) tc::tmem_ld_32x32b_x8(ta, v), tc::tmem_ld_32x32b_x8(ta + RP, l);
+      else tc::tmem_ld_32x32b_x16(ta, v), tc::tmem_ld_32x32b_x16(ta + RP, l);
       tc::tmem_ld_wait();
 #pragma unroll
       for (int e = 0; e < CW; ++e)
         sums[(hf * HC + q + e) * GT_LD + col] =
-            !ok ? __int_as_float(0x7fc00000) : base > 0 ? v[e] : 0.f;
+            !ok ? __int_as_float(0x7fc00000) : base > 0 ? v[e] + l[e] : 0.f;
     }
   }
   tc::tc_fence_before();
