@@ -269,164 +269,32 @@ def rotate(x, signs, block, out, inverse=False, stream=None):
     _check(st, "gptq_rotate")
 
 
-def _invalid(where: str, detail: str):
-    raise GptqError(GPTQ_ERR_INVALID_ARG, where, detail)
+_ops = None
 
 
-# The operators below check every tensor's type, shape, strides and device in Python, since
-# the C ABI sees addresses only.  For a single token these checks cost as much as the
-# kernel, so they are written for few attribute reads.
+def ops():
+    """The extension module of the adapter, checkpoint and input-gradient operators
+    (csrc_py/ops.cpp: argument checks and allocation, then the C ABI).  Raises if
+    it has not been built."""
+    global _ops
+    if _ops is None:
+        load()
+        try:
+            from . import _ops as module
+        except ImportError as e:
+            raise ImportError(f"the extension module _ops is not built ({e}); run "
+                              "`python -m post_weight_quantization_23_b200.build`") from e
+        module.set_error(GptqError)
+        _ops = module
+    return _ops
 
 
-def _device(where, first, *rest):
-    """The CUDA device that all tensors share (None entries are left out)."""
-    dev = first.get_device()
-    if dev < 0:
-        _invalid(where, "tensor not on a CUDA device")
-    for t in rest:
-        if t is not None and t.get_device() != dev:
-            _invalid(where, "tensors on different devices")
-    return dev
-
-
-def _call(where, dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current (the library launches on the current device),
-    on the given stream or that device's current one."""
+def on_stream(where, stream, first, fn, *args):
+    """fn(*args) on the current stream, or on `stream`: then what it allocates belongs to
+    that stream (the caching allocator reuses the memory in its order)."""
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        if stream.device.index != dev:
-            _invalid(where, "stream of another device")
-        s = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, s)
-    if st != GPTQ_OK:
-        raise GptqError(st, where)
-
-
-def _rows(where, name, t, rows, cols, dtype):
-    """A (rows, cols) matrix of dtype with unit column stride; its leading dimension."""
-    if t.dtype is not dtype or t.shape != (rows, cols):
-        _invalid(where, f"{name}: {tuple(t.shape)} {t.dtype}, want ({rows}, {cols}) {dtype}")
-    ld, cs = t.stride()
-    if cs != 1 and cols > 1:
-        _invalid(where, f"{name}: unit column stride")
-    return ld if rows > 1 and cols > 0 else max(ld, cols, 1)
-
-
-def _whole(where, name, t, shape, dtype):
-    """A contiguous tensor of the given shape and dtype; its address."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _invalid(where, f"{name}: {tuple(t.shape)} {t.dtype}, want contiguous {shape} {dtype}")
-    return t.data_ptr()
-
-
-def gemm_dgrad(dY, qweight, scales, zeros, g_idx, bits, group_size, k, dX, stream=None):
-    """dX = dY W_hat from the packed weights (gptq_gemm_dgrad)."""
-    w = "gptq_gemm_dgrad"
-    if dY.dim() != 2 or scales.dim() != 2:
-        _invalid(w, "dY (m, n), scales (n, ngroups)")
-    m, n = dY.shape
-    ng = scales.shape[1]
-    dtype = dY.dtype
-    dt = dtype_code(dtype)
-    if bits not in (2, 3, 4, 8):
-        raise GptqError(GPTQ_ERR_UNSUPPORTED, w, f"bits {bits}")
-    ldy, ldx = _rows(w, "dY", dY, m, n, dtype), _rows(w, "dX", dX, m, k, dtype)
-    qw = _whole(w, "qweight", qweight, (n, k * bits // 32), torch.int32)
-    sc = _whole(w, "scales", scales, (n, ng), torch.float32)
-    ze = _whole(w, "zeros", zeros, (n, ng), torch.int32)
-    gi = _whole(w, "g_idx", g_idx, (k,), torch.int32) if g_idx is not None else None
-    dev = _device(w, dY, qweight, scales, zeros, g_idx, dX)
-    _call(w, dev, stream, load().gptq_gemm_dgrad, dY.data_ptr(), dt, m, n, ldy, qw, sc, ze, gi, k,
-          bits, group_size, ng, dX.data_ptr(), ldx)
-
-
-def _adapters(w, A, B, scaling, starts, adapter, dtype):
-    """Checks the adapters and the requests; sizes (na, rank, k, n, nreq) and addresses."""
-    if A.dim() != 3 or B.dim() != 3 or adapter.dim() != 1:
-        _invalid(w, "A (na, rank, k), B (na, n, rank), adapter (requests,)")
-    na, r, k = A.shape
-    n = B.shape[1]
-    nreq = len(adapter)
-    return na, r, k, n, nreq, (
-        _whole(w, "A", A, (na, r, k), dtype), _whole(w, "B", B, (na, n, r), dtype),
-        _whole(w, "scaling", scaling, (na,), torch.float32),
-        _whole(w, "starts", starts, (nreq + 1,), torch.int32),
-        _whole(w, "adapter", adapter, (nreq,), torch.int32))
-
-
-def lora_add(Y, X, A, B, scaling, starts, adapter, out, V=None, stream=None):
-    """out = Y + B_a (scaling_a A_a x) for every row of every request (gptq_lora_add)."""
-    w = "gptq_lora_add"
-    dtype = X.dtype
-    dt = dtype_code(dtype)
-    na, r, k, n, nreq, (pa, pb, ps, pst, pad) = _adapters(w, A, B, scaling, starts, adapter, dtype)
-    m = len(X)
-    ldx, ldo = _rows(w, "X", X, m, k, dtype), _rows(w, "out", out, m, n, dtype)
-    po = out.data_ptr()
-    if Y is None:
-        py, ldy = None, 0
-    elif Y is out:
-        py, ldy = po, ldo
-    else:
-        py, ldy = Y.data_ptr(), _rows(w, "Y", Y, m, n, dtype)
-    pv = _whole(w, "V", V, (m, r), torch.float32) if V is not None else None
-    dev = _device(w, X, Y, A, B, scaling, starts, adapter, out, V)
-    _call(w, dev, stream, load().gptq_lora_add, py, ldy, X.data_ptr(), dt, m, k, ldx, pa, pb, ps, na,
-          r, pst, pad, nreq, n, po, ldo, pv)
-
-
-def lora_backward(dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB, ws,
-                  stream=None):
-    """The adapters' gradients and out = dX + A_a^T U (gptq_lora_backward)."""
-    w = "gptq_lora_backward"
-    dtype = dY.dtype
-    dt = dtype_code(dtype)
-    na, r, k, n, nreq, (pa, pb, ps, pst, pad) = _adapters(w, A, B, scaling, starts, adapter, dtype)
-    m = len(dY)
-    ldy = _rows(w, "dY", dY, m, n, dtype)
-    ldx = _rows(w, "X", X, m, k, dtype if x_scales is None else torch.int8)
-    xs = None
-    if x_scales is not None:
-        xs = _whole(w, "x_scales", x_scales, (m, (k + 127) // 128), torch.float32)
-    pv = _whole(w, "V", V, (m, r), torch.float32)
-    pdx, ldd, po, ldo = None, 0, None, 0
-    if out is not None:
-        po, ldo = out.data_ptr(), _rows(w, "out", out, m, k, dtype)
-        if dX is out:
-            pdx, ldd = po, ldo
-        elif dX is not None:
-            pdx, ldd = dX.data_ptr(), _rows(w, "dX", dX, m, k, dtype)
-    da, db = _whole(w, "dA", dA, (na, r, k), dtype), _whole(w, "dB", dB, (na, n, r), dtype)
-    dev = _device(w, dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB, ws)
-    _call(w, dev, stream, load().gptq_lora_backward, dY.data_ptr(), dt, m, n, ldy, X.data_ptr(), ldx,
-          xs, k, pv, pa, pb, ps, na, r, pst, pad, nreq, pdx, ldd, po, ldo, da, db, ws.data_ptr(),
-          ws.nbytes)
-
-
-def act_checkpoint(X, codes, scales, stream=None):
-    """8-bit codes and block scales of X (gptq_act_checkpoint)."""
-    w = "gptq_act_checkpoint"
-    m, k = X.shape
-    dtype = X.dtype
-    dt = dtype_code(dtype)
-    ldx, ldc = _rows(w, "X", X, m, k, dtype), _rows(w, "codes", codes, m, k, torch.int8)
-    sp = _whole(w, "scales", scales, (m, (k + 127) // 128), torch.float32)
-    _call(w, _device(w, X, codes, scales), stream, load().gptq_act_checkpoint, X.data_ptr(), dt, m, k,
-          ldx, codes.data_ptr(), ldc, sp)
-
-
-def act_restore(codes, scales, out, stream=None):
-    """The activations of a checkpoint (gptq_act_restore)."""
-    w = "gptq_act_restore"
-    m, k = codes.shape
-    dtype = out.dtype
-    dt = dtype_code(dtype)
-    ldc, ldo = _rows(w, "codes", codes, m, k, torch.int8), _rows(w, "out", out, m, k, dtype)
-    sp = _whole(w, "scales", scales, (m, (k + 127) // 128), torch.float32)
-    _call(w, _device(w, codes, scales, out), stream, load().gptq_act_restore, codes.data_ptr(), ldc,
-          sp, m, k, dt, out.data_ptr(), ldo)
+        return fn(*args)
+    if stream.device.index != first.get_device():
+        raise GptqError(GPTQ_ERR_INVALID_ARG, where, "stream of another device")
+    with torch.cuda.stream(stream):
+        return fn(*args)

@@ -196,15 +196,6 @@ def quant_matmul(X: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
     return out
 
 
-def _empty(dtype, device, stream, *shape):
-    """A new tensor that belongs to the stream the call runs on (the caching
-    allocator reuses its memory in that stream's order)."""
-    if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(*shape, dtype=dtype, device=device)
-
-
 def quant_matmul_dgrad(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
                        zeros: torch.Tensor, bits: int, group_size: int, k: int, g_idx=None,
                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -212,10 +203,8 @@ def quant_matmul_dgrad(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     straight from the packed weights (gptq_gemm_dgrad): dY (m, n) f16/bf16 on the
     device, the weights as for quant_matmul.  Returns dX (m, k) in dY's dtype
     (``out`` if given)."""
-    if out is None:
-        out = _empty(dY.dtype, dY.device, stream, len(dY), k)
-    _lib.gemm_dgrad(dY, qweight, scales, zeros, g_idx, bits, group_size, k, out, stream)
-    return out
+    return _lib.on_stream("gptq_gemm_dgrad", stream, dY, (_lib._ops or _lib.ops()).gemm_dgrad, dY,
+                          qweight, scales, zeros, bits, group_size, k, g_idx, out)
 
 
 def lora_add(Y, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: torch.Tensor,
@@ -232,12 +221,8 @@ def lora_add(Y, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: torc
     given.  ``V`` (m, rank) fp32, if given, receives scaling_a A_a x_t, which
     lora_backward needs.  Rows outside the requests are left as they are.
     Returns the updated tensor."""
-    if out is None:
-        if Y is None:
-            raise GptqError(_lib.GPTQ_ERR_INVALID_ARG, "gptq_lora_add", "Y or out")
-        out = Y
-    _lib.lora_add(Y, X, A, B, scaling, starts, adapter, out, V, stream)
-    return out
+    return _lib.on_stream("gptq_lora_add", stream, X, (_lib._ops or _lib.ops()).lora_add, Y, X, A, B,
+                          scaling, starts, adapter, out, V)
 
 
 def lora_backward(dY: torch.Tensor, X: torch.Tensor, V: torch.Tensor, A: torch.Tensor,
@@ -255,18 +240,8 @@ def lora_backward(dY: torch.Tensor, X: torch.Tensor, V: torch.Tensor, A: torch.T
     Without ``out`` dX is updated in place; with neither, no input gradient is
     formed.  ``ws`` is scratch memory of workspace_size(OP_LORA_BACKWARD, rank,
     0, m) bytes, allocated here if not given.  Returns (out, dA, dB)."""
-    if out is None:
-        out = dX
-    if dA is None:
-        dA = _empty(A.dtype, A.device, stream, *A.shape)
-    if dB is None:
-        dB = _empty(B.dtype, B.device, stream, *B.shape)
-    if ws is None:
-        nbytes = _lib.workspace_size(_lib.OP_LORA_BACKWARD, A.shape[1], 0, len(dY), None)
-        ws = _empty(torch.uint8, dY.device, stream, max(nbytes, 1))
-    _lib.lora_backward(dY, X, x_scales, V, A, B, scaling, starts, adapter, dX, out, dA, dB, ws,
-                       stream)
-    return out, dA, dB
+    return _lib.on_stream("gptq_lora_backward", stream, dY, (_lib._ops or _lib.ops()).lora_backward,
+                          dY, X, V, A, B, scaling, starts, adapter, dX, x_scales, out, dA, dB, ws)
 
 
 def act_checkpoint(X: torch.Tensor, codes: torch.Tensor | None = None,
@@ -274,23 +249,16 @@ def act_checkpoint(X: torch.Tensor, codes: torch.Tensor | None = None,
     """Activations (m, k) f32/f16/bf16 kept in 8 bits for a backward pass
     (gptq_act_checkpoint): int8 codes (m, k) and fp32 scales (m, ceil(k/128)),
     one per row and block of 128 columns.  Returns (codes, scales)."""
-    m, k = X.shape
-    if codes is None:
-        codes = _empty(torch.int8, X.device, stream, m, k)
-    if scales is None:
-        scales = _empty(torch.float32, X.device, stream, m, (k + 127) // 128)
-    _lib.act_checkpoint(X, codes, scales, stream)
-    return codes, scales
+    return _lib.on_stream("gptq_act_checkpoint", stream, X, (_lib._ops or _lib.ops()).act_checkpoint,
+                          X, codes, scales)
 
 
 def act_restore(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.float16,
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The activations that act_checkpoint kept, codes * scales (gptq_act_restore),
     in ``dtype`` (or into ``out``)."""
-    if out is None:
-        out = _empty(dtype, codes.device, stream, *codes.shape)
-    _lib.act_restore(codes, scales, out, stream)
-    return out
+    return _lib.on_stream("gptq_act_restore", stream, codes, (_lib._ops or _lib.ops()).act_restore,
+                          codes, scales, dtype, out)
 
 
 def hadamard_block(k: int, largest: int = 8192) -> int:

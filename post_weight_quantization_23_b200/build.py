@@ -3,18 +3,23 @@
     python -m post_weight_quantization_23_b200.build [--verbose-ptxas]
 
 Every .cu under csrc/ is compiled for sm_100a and linked into one shared
-library next to this file; the Python binding loads that file only.
+library next to this file.  csrc_py/ops.cpp, the Python entry of the adapter,
+checkpoint and input-gradient operators, becomes the extension module _ops beside
+it (g++ against torch's headers; it calls the library's C ABI).
 """
 import argparse
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgptq_b200.so")
 OBJ = os.path.join(HERE, "_build")
+OPS_SRC = os.path.join(HERE, "csrc_py", "ops.cpp")
+OPS = os.path.join(HERE, "_ops" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -64,7 +69,26 @@ def build(verbose_ptxas=False, force=False, jobs=None):
         cmd = [nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs,
                "-o", LIB]
         subprocess.run(cmd, check=True)
+    build_ops(force)
     return LIB
+
+
+def build_ops(force=False):
+    deps = [OPS_SRC, os.path.join(HERE, "..", "include", "gptq.h"), os.path.abspath(__file__)]
+    if (not force and os.path.exists(OPS)
+            and os.path.getmtime(OPS) >= max(os.path.getmtime(d) for d in deps)):
+        return OPS
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    tlib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    incs = [*include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{i}" for i in incs], OPS_SRC, "-o", OPS, "-L" + HERE, "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN", "-L" + tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    subprocess.run(cmd, check=True)
+    return OPS
 
 
 if __name__ == "__main__":
