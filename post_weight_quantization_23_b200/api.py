@@ -118,6 +118,13 @@ class GptqPlan:
         return quant_matmul(X, self.qweight, self.scales, self.zeros, self.cfg.bits,
                             self.cfg.group_size, g_idx, out, stream)
 
+    def matmul_dgrad(self, dY: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        """dX = dY W_hat with this plan's packed weights: the gradient of matmul with
+        respect to its input (quant_matmul_dgrad)."""
+        g_idx = self.g_idx if (self.cfg.act_order and not self.cfg.static_groups) else None
+        return quant_matmul_dgrad(dY, self.qweight, self.scales, self.zeros, self.cfg.bits,
+                                  self.cfg.group_size, self.k, g_idx, out, stream)
+
     def run_after_hessian(self, W: torch.Tensor, stream=None):
         """prepare -> quantize -> pack -> dequant, no synchronisation."""
         self.prepare(stream)

@@ -400,7 +400,9 @@ lora_grad_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant
                                       ad);
   }
   // all MMAs done (their stages are free for the sums), all copies landed
-  if (warp == 1 && lane == 0) tc::mma_commit(done);
+  if (warp == 1) {
+    if (tc::elect_one()) tc::mma_commit(done);  // the lane that issued them
+  }
   const bool finished = tc::mbar_wait_warp(done, 0, abort_flag, tc::kSpinLimit);
   if (*abort_flag && threadIdx.x == 0)
     for (int p = max(0, *issued - R); p < *issued; ++p)

@@ -509,10 +509,13 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     cluster_wait();
     tc::tc_fence_after();
     if (*abort_flag) {  // the outputs of what this cluster had left become NaN
-      if (warp == 1 && lane == 0) {  // every MMA issued above finishes before TMEM goes
-        tc::mma_commit(done);
-        for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
-          if (tc::mbar_try_wait(done, 0)) break;
+      if (warp == 1) {  // every MMA issued above finishes before TMEM goes
+        if (tc::elect_one()) {  // the lane that issued them
+          tc::mma_commit(done);
+          for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
+            if (tc::mbar_try_wait(done, 0)) break;
+        }
+        __syncwarp();
       }
       if (threadIdx.x == 0)  // the copies in flight land before the shared memory goes
         for (int p = max(0, *issued - S); p < *issued; ++p)

@@ -392,3 +392,105 @@ def test_repeats_under_load(dtype, r):
         for x, y in zip(got + (out, s["V"]), first[saved] + (first_y, V)):
             bad += (x != y).any()
     assert int(bad) == 0
+
+
+# ---------------------------------------------------------------- long and crowded batches
+
+
+@pytest.mark.parametrize("r,m,k,n", [(8, 140000, 64, 64), (128, 10000, 64, 136), (64, 20000, 72, 64)])
+def test_many_pieces_per_cluster(r, m, k, n):
+    # more pieces than the clusters take at once, more tiles than one look-up holds
+    from post_weight_quantization_23_b200 import act_checkpoint, lora_add, lora_backward
+    lens = [m // 2 + 1, 3, m - m // 2 - 4 - 77, 77]
+    s = R.make(BF, k, n, r, 2, lens, [0, 1, 1, 0], r)
+    ref, bound, Vr, bv, cov = R.add_ref(s, BF)
+    V = torch.zeros(m, r, device="cuda")
+    out = lora_add(s["Y"], s["X"], s["A"], s["B"], s["scaling"], s["starts"], s["adapter"],
+                   out=torch.empty_like(s["Y"]), V=V)
+    R.check(out, ref, bound, "out")
+    R.check(V, Vr, bv, "V")
+    s["V"] = V
+    for saved in (16, 8):
+        X, xs, Xd = s["X"], None, s["X"].to(R.D)
+        if saved == 8:
+            X, xs = act_checkpoint(s["X"])
+            Xd = X.to(R.D) * xs.to(R.D).repeat_interleave(128, 1)[:, :k]
+        b = R.backward_ref(s, BF, Xd)
+        got = lora_backward(s["dY"], X, V, s["A"], s["B"], s["scaling"], s["starts"], s["adapter"],
+                            s["dX"], x_scales=xs, out=torch.empty_like(s["dX"]))
+        for g, name in zip(got, ("out", "dA", "dB")):
+            R.check(g, *b[name], name)
+
+
+@pytest.mark.parametrize("dtype", [H, BF])
+def test_add_many_requests(dtype):
+    # 1001 requests over 37 adapters: several windows of the decode kernel, pieces that gather
+    # tokens of many requests, some long ones among them
+    from post_weight_quantization_23_b200 import lora_add
+    g = torch.Generator().manual_seed(1)
+    lens = torch.randint(0, 4, (1001,), generator=g).tolist()
+    lens[500], lens[77] = 300, 40
+    ids = torch.randint(-1, 38, (1001,), generator=g).tolist()
+    s = R.make(dtype, 256, 328, 16, 37, lens, ids, 3, first=1, tail=2)
+    ref, bound, Vr, bv, cov = R.add_ref(s, dtype)
+    V = torch.full((s["X"].shape[0], 16), 5.0, device="cuda")
+    out = torch.full_like(s["Y"], 7.0)
+    lora_add(s["Y"], s["X"], s["A"], s["B"], s["scaling"], s["starts"], s["adapter"], out=out, V=V)
+    R.check(out[cov], ref[cov], bound[cov], "out")
+    R.check(V[cov], Vr[cov], bv[cov], "V")
+    assert (out[~cov] == 7.0).all() and (V[~cov] == 5.0).all()
+
+
+def test_backward_many_requests_and_adapters():
+    from post_weight_quantization_23_b200 import lora_backward
+    g = torch.Generator().manual_seed(2)
+    lens = torch.randint(0, 90, (300,), generator=g).tolist()
+    ids = torch.randint(-1, 10, (300,), generator=g).tolist()
+    s = R.make(H, 136, 200, 16, 9, lens, ids, 5)
+    _with_v(s, H)
+    ref = R.backward_ref(s, H, s["X"].to(R.D))
+    got = lora_backward(s["dY"], s["X"], s["V"], s["A"], s["B"], s["scaling"], s["starts"],
+                        s["adapter"], s["dX"], out=torch.empty_like(s["dX"]))
+    for x, name in zip(got, ("out", "dA", "dB")):
+        R.check(x, *ref[name], name)
+
+
+def test_backward_unaligned_v():
+    # V on a 4-byte boundary: the general gradient kernel
+    from post_weight_quantization_23_b200 import lora_backward
+    s = R.make(BF, 128, 64, 8, 1, [90], [0], 5)
+    _with_v(s, BF)
+    buf = torch.zeros(90 * 8 + 1, device="cuda")
+    V = buf[1:].view(90, 8)
+    V.copy_(s["V"])
+    ref = R.backward_ref(s, BF, s["X"].to(R.D))
+    got = lora_backward(s["dY"], s["X"], V, s["A"], s["B"], s["scaling"], s["starts"], s["adapter"],
+                        s["dX"].clone())
+    for x, name in zip(got, ("out", "dA", "dB")):
+        R.check(x, *ref[name], name)
+
+
+def test_two_streams_at_once():
+    # two backward passes and a forward call side by side, each with its own workspace
+    from post_weight_quantization_23_b200 import lora_add, lora_backward
+    ss = []
+    for i in range(2):
+        s = R.make(BF, 1024, 1024, 32, 2, [700, 400], [0, 1], i)
+        _with_v(s, BF)
+        a = (s["A"], s["B"], s["scaling"], s["starts"], s["adapter"])
+        want = lora_backward(s["dY"], s["X"], s["V"], *a, s["dX"], out=torch.empty_like(s["dX"]))
+        y = lora_add(s["Y"], s["X"], *a, out=torch.empty_like(s["Y"]))
+        ss.append((s, a, want, y))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        for (s, a, want, y), st in zip(ss, streams):
+            with torch.cuda.stream(st):
+                o = lora_backward(s["dY"], s["X"], s["V"], *a, s["dX"], out=torch.empty_like(s["dX"]))
+                got.append(o + (lora_add(s["Y"], s["X"], *a, out=torch.empty_like(s["Y"])),))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        _, _, want, y = ss[i % 2]
+        for p, q in zip(o, want + (y,)):
+            assert torch.equal(p, q)

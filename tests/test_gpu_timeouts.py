@@ -131,3 +131,59 @@ def test_inference_product_wait_gives_up_with_nan_outputs():
     ref = O.dequant_matmul(X.double().cpu().numpy(), qw.cpu().numpy(), sc.cpu().numpy(),
                            z.cpu().numpy().astype(np.int64), np.arange(k) // G, 4, k)
     assert np.abs(Y.double().cpu().numpy() - ref).max() <= 4e-3 * np.abs(ref).max()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("r", [16, 128])
+def test_adapters_give_up_and_recover(dtype, r):
+    # the adapters' tensor-core kernels write NaN over the rows that have an adapter, leave the
+    # others, and the next call is right again
+    import _adapters as R
+    from post_weight_quantization_23_b200 import act_checkpoint, lora_add, lora_backward
+    s = R.make(dtype, 512, 1000, r, 2, [300, 40, 500], [0, -1, 1], r, first=2, tail=3)
+    a = (s["A"], s["B"], s["scaling"], s["starts"], s["adapter"])
+    ref, bound, Vr, bv, cov = R.add_ref(s, dtype)
+    own = cov.clone()
+    own[302:342] = False
+    V = torch.zeros(s["X"].shape[0], r, device="cuda")
+    with _Limit(0):
+        out = lora_add(s["Y"], s["X"], *a, out=torch.full_like(s["Y"], 7.0), V=V)
+        torch.cuda.synchronize()
+    assert out[own].isnan().all() and V[own].isnan().all()
+    assert torch.equal(out[302:342], s["Y"][302:342]) and (out[~cov] == 7.0).all()
+    out = lora_add(s["Y"], s["X"], *a, out=torch.full_like(s["Y"], 7.0), V=V)
+    R.check(out[cov], ref[cov], bound[cov], "out")
+    R.check(V[cov], Vr[cov], bv[cov], "V")
+    s["V"] = V
+    codes, xs = act_checkpoint(s["X"])
+    for X, sc in ((s["X"], None), (codes, xs)):
+        with _Limit(0):
+            dX, dA, dB = lora_backward(s["dY"], X, V, *a, s["dX"], x_scales=sc,
+                                       out=torch.full_like(s["dX"], 7.0))
+            torch.cuda.synchronize()
+        assert dX[own].isnan().all() and (dX[~cov] == 7.0).all()
+        assert dA.isnan().all() and dB.isnan().all()
+        Xd = X.to(R.D) if sc is None else X.to(R.D) * sc.to(R.D).repeat_interleave(128, 1)
+        b = R.backward_ref(s, dtype, Xd)
+        got = lora_backward(s["dY"], X, V, *a, s["dX"], x_scales=sc, out=torch.full_like(s["dX"], 7.0))
+        R.check(got[0][cov], b["out"][0][cov], b["out"][1][cov], "dX")
+        R.check(got[1], *b["dA"], "dA")
+        R.check(got[2], *b["dB"], "dB")
+
+
+@pytest.mark.parametrize("m", [100, 700])
+def test_dgrad_gives_up_and_recovers(m):
+    from post_weight_quantization_23_b200 import quant_matmul_dgrad
+    g = torch.Generator(device="cuda").manual_seed(m)
+    n, k = 512, 768
+    qw = torch.randint(-2 ** 31, 2 ** 31, (n, k // 8), generator=g, device="cuda").to(torch.int32)
+    sc = torch.rand(n, k // 128, generator=g, device="cuda") * 0.02
+    ze = torch.full((n, k // 128), 8, dtype=torch.int32, device="cuda")
+    dY = torch.randn(m, n, generator=g, device="cuda").half()
+    want = quant_matmul_dgrad(dY, qw, sc, ze, 4, 128, k)
+    assert torch.isfinite(want).all()
+    with _Limit(0):
+        bad = quant_matmul_dgrad(dY, qw, sc, ze, 4, 128, k)
+        torch.cuda.synchronize()
+    assert bad.isnan().all()
+    assert torch.equal(quant_matmul_dgrad(dY, qw, sc, ze, 4, 128, k), want)
