@@ -97,8 +97,10 @@ __device__ __forceinline__ void ld_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ld_nc_u4(const void* p) {
-  return __ldg(reinterpret_cast<const uint4*>(p));
+// Every load of this kernel goes to L2 (cache-global): beside the tensor-core kernel it
+// starts without waiting for it (see `late`), so no L1 line of an earlier kernel may serve.
+__device__ __forceinline__ uint4 ld_u4(const void* p) {
+  return __ldcg(reinterpret_cast<const uint4*>(p));
 }
 
 // A piece is up to 8 rows of one adapter, of one request or of several (a batch of single
@@ -121,7 +123,7 @@ __device__ __forceinline__ LdWindow ld_window(const LoraArgs& a, int q0, LdShare
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = q0 + tid;
   LdWindow w = {0, 0, -1, 0, 0, 0, 0};
   if (q < a.nreq) {
-    const int b = a.starts[q], e = a.starts[q + 1], ad = a.adapter[q];
+    const int b = __ldcg(a.starts + q), e = __ldcg(a.starts + q + 1), ad = __ldcg(a.adapter + q);
     w.start = lora_clamp(b, a.m);
     w.len = lora_clamp(e, a.m) - w.start;
     if (w.len < a.min_len || w.len > a.max_len) w.len = 0;
@@ -191,7 +193,7 @@ __device__ __forceinline__ int ld_piece(const LdWindow& w, int p, LdShared& sm) 
 // time, the first of them before the barrier.  One launch, no workspace, sums in a fixed order.
 template <bool BF16, int RP>
 __global__ void __launch_bounds__(LD_THREADS, RP <= 32 ? 3 : RP == 64 ? 2 : 1)
-lora_decode_kernel(LoraArgs a, int yvec) {
+lora_decode_kernel(LoraArgs a, int yvec, int late) {
   using Ty = LoraType<BF16>;
   using T = typename Ty::T;
   constexpr int MT = RP / 16;                  // 16-row tiles of the rank
@@ -215,7 +217,11 @@ lora_decode_kernel(LoraArgs a, int yvec) {
   constexpr int NW = LORA_CLUSTER * LD_WARPS;
   const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
   cluster_arrive();  // this CTA runs: peers may write to its shared memory
-  pdl_wait();
+  // late: the kernel before this one is the tensor-core kernel of the same call, on other
+  // rows.  All of its CTAs had waited for the kernels before the call when this one could
+  // start, so this one runs beside it and waits for it before it ends: whatever follows
+  // then finds both done.
+  if (!late) pdl_wait();
   pdl_trigger();
   bool waited = false;
   int turn = 0;
@@ -255,17 +261,17 @@ lora_decode_kernel(LoraArgs a, int yvec) {
       for (int c0 = gw * 64; c0 < a.K; c0 += NW * 64) {
         const int ca = c0 + 8 * t, cb = ca + 32;
         const bool oka = ca < a.K, okb = cb < a.K;
-        const uint4 xa = tok && oka ? ld_nc_u4(xrow + ca) : zero4;
-        const uint4 xb = tok && okb ? ld_nc_u4(xrow + cb) : zero4;
+        const uint4 xa = tok && oka ? ld_u4(xrow + ca) : zero4;
+        const uint4 xb = tok && okb ? ld_u4(xrow + cb) : zero4;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           const int p0 = 16 * i + g, p1 = p0 + 8;
           const T* r0 = A + (int64_t)p0 * a.K;
           const T* r1 = A + (int64_t)p1 * a.K;
-          const uint4 a0 = p0 < a.r && oka ? ld_nc_u4(r0 + ca) : zero4;
-          const uint4 a1 = p1 < a.r && oka ? ld_nc_u4(r1 + ca) : zero4;
-          const uint4 b0 = p0 < a.r && okb ? ld_nc_u4(r0 + cb) : zero4;
-          const uint4 b1 = p1 < a.r && okb ? ld_nc_u4(r1 + cb) : zero4;
+          const uint4 a0 = p0 < a.r && oka ? ld_u4(r0 + ca) : zero4;
+          const uint4 a1 = p1 < a.r && oka ? ld_u4(r1 + ca) : zero4;
+          const uint4 b0 = p0 < a.r && okb ? ld_u4(r0 + cb) : zero4;
+          const uint4 b1 = p1 < a.r && okb ? ld_u4(r1 + cb) : zero4;
           ld_mma<BF16>(acc[i], a0.x, a1.x, a0.y, a1.y, xa.x, xa.y);
           ld_mma<BF16>(acc[i], a0.z, a1.z, a0.w, a1.w, xa.z, xa.w);
           ld_mma<BF16>(acc[i], b0.x, b1.x, b0.y, b1.y, xb.x, xb.y);
@@ -287,18 +293,18 @@ lora_decode_kernel(LoraArgs a, int yvec) {
             const T* q0 = B + (int64_t)(ju + g) * a.r + p;
             const T* q1 = q0 + (int64_t)8 * a.r;
             if (RP >= 32) {
-              w0[u][c] = ok0 ? ld_nc_u4(q0) : zero4;
-              w1[u][c] = ok1 ? ld_nc_u4(q1) : zero4;
+              w0[u][c] = ok0 ? ld_u4(q0) : zero4;
+              w1[u][c] = ok1 ? ld_u4(q1) : zero4;
             } else {
-              const uint2 u0 = ok0 ? __ldg((const uint2*)q0) : make_uint2(0u, 0u);
-              const uint2 u1 = ok1 ? __ldg((const uint2*)q1) : make_uint2(0u, 0u);
+              const uint2 u0 = ok0 ? __ldcg((const uint2*)q0) : make_uint2(0u, 0u);
+              const uint2 u1 = ok1 ? __ldcg((const uint2*)q1) : make_uint2(0u, 0u);
               w0[u][c] = make_uint4(u0.x, u0.y, 0u, 0u);
               w1[u][c] = make_uint4(u1.x, u1.y, 0u, 0u);
             }
           }
           const int j = ju + 4 * t;
           yv[u] = tok && yvec && a.Y != nullptr && j + 4 <= a.N
-                      ? *reinterpret_cast<const uint2*>(Y + row * a.ldy + j)
+                      ? __ldcg(reinterpret_cast<const uint2*>(Y + row * a.ldy + j))
                       : make_uint2(0u, 0u);
         }
       };
@@ -332,7 +338,7 @@ lora_decode_kernel(LoraArgs a, int yvec) {
       cluster_arrive();
       cluster_wait();
       // (a peer writes to this half of parts again only after the next piece's barrier)
-      const float sc = a.scaling[ad];
+      const float sc = __ldcg(a.scaling + ad);
       float* vs = red;  // V of the piece, [token][RP]
       for (int e = tid; e < PS; e += LD_THREADS) {
         float s = 0.f;
@@ -408,7 +414,8 @@ lora_decode_kernel(LoraArgs a, int yvec) {
               const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (j + i < a.N) op[i] = Ty::cvt((a.Y != nullptr ? to_f32(yp[i]) : 0.f) + e[i]);
+                if (j + i < a.N)
+                  op[i] = Ty::cvt((a.Y != nullptr ? to_f32(__ldcg(yp + i)) : 0.f) + e[i]);
             }
           }
           __syncwarp();
@@ -418,10 +425,11 @@ lora_decode_kernel(LoraArgs a, int yvec) {
     base += win.total;
   }
   if (!waited) cluster_wait();
+  if (late) pdl_wait();
 }
 
 template <bool BF16, int RP>
-gptq_status launch_decode(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
+gptq_status launch_decode(const LoraArgs& a, int64_t pieces, bool late, cudaStream_t s) {
   // rows of Y and out on 16-byte (2) or 8-byte (1) boundaries
   auto on = [&](int bytes) {
     return (uintptr_t)a.Y % bytes == 0 && (uintptr_t)a.out % bytes == 0 &&
@@ -438,17 +446,17 @@ gptq_status launch_decode(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
   pieces = std::min<int64_t>(pieces, resident_clusters((const void*)lora_decode_kernel<BF16, RP>,
                                                        LORA_CLUSTER, LD_THREADS, smem));
   launch_cluster_pdl(lora_decode_kernel<BF16, RP>, dim3((unsigned)(pieces * LORA_CLUSTER)),
-                     dim3(LD_THREADS), smem, LORA_CLUSTER, s, a, yvec);
+                     dim3(LD_THREADS), smem, LORA_CLUSTER, s, a, yvec, (int)late);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
 
 template <bool BF16>
-gptq_status decode_ranks(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
-  if (a.r <= 16) return launch_decode<BF16, 16>(a, pieces, s);
-  if (a.r <= 32) return launch_decode<BF16, 32>(a, pieces, s);
-  if (a.r <= 64) return launch_decode<BF16, 64>(a, pieces, s);
-  return launch_decode<BF16, 128>(a, pieces, s);
+gptq_status decode_ranks(const LoraArgs& a, int64_t pieces, bool late, cudaStream_t s) {
+  if (a.r <= 16) return launch_decode<BF16, 16>(a, pieces, late, s);
+  if (a.r <= 32) return launch_decode<BF16, 32>(a, pieces, late, s);
+  if (a.r <= 64) return launch_decode<BF16, 64>(a, pieces, late, s);
+  return launch_decode<BF16, 128>(a, pieces, late, s);
 }
 
 bool rows16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
@@ -476,17 +484,18 @@ gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
   if (!rows16(a.X, a.ldx) || !rows16(a.P, a.K) || !rows16(a.Q, a.r))
     return lora_general(a, bf16, false, s);
   const bool tc = a.m > LORA_DECODE_ROWS && lora_tc_supported(a, false);
-  if (!tc || a.nreq > 1) {
-    if (tc) a.max_len = LORA_SHORT;
-    const int64_t pieces = std::min<int64_t>(
-        std::min<int64_t>(a.m, (int64_t)a.m / LD_TT + a.nreq), a.nreq * cdiv(a.max_len, LD_TT));
-    const gptq_status st =
-        bf16 ? decode_ranks<true>(a, pieces, s) : decode_ranks<false>(a, pieces, s);
-    if (st != GPTQ_OK || !tc) return st;
-    a.min_len = LORA_SHORT + 1;
-    a.max_len = a.m;
+  if (tc) {
+    // the long requests first, the short ones beside them on the SMs that are left
+    if (a.nreq > 1) a.min_len = LORA_SHORT + 1;
+    const gptq_status st = lora_tc(a, bf16, false, s);
+    if (st != GPTQ_OK || a.nreq == 1) return st;
+    a.min_len = 1;
+    a.max_len = LORA_SHORT;
   }
-  return lora_tc(a, bf16, false, s);
+  const int64_t pieces =
+      std::min<int64_t>(std::min<int64_t>(a.m, (int64_t)a.m / LD_TT + a.nreq),
+                        a.nreq * cdiv(std::min(a.max_len, a.m), LD_TT));
+  return bf16 ? decode_ranks<true>(a, pieces, tc, s) : decode_ranks<false>(a, pieces, tc, s);
 }
 
 // U = scaling B^T dY and, where a.out is set, out = Y + A^T U.

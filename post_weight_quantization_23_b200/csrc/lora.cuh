@@ -255,7 +255,7 @@ __device__ __forceinline__ void lora_copy_row(const T* y, T* o, int j0, int j1, 
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const int j = b + 256 * q + 8 * lane;
-        w[q] = y != nullptr && j + 8 <= j1 ? *reinterpret_cast<const uint4*>(y + j)
+        w[q] = y != nullptr && j + 8 <= j1 ? __ldcg(reinterpret_cast<const uint4*>(y + j))
                                            : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
@@ -268,7 +268,7 @@ __device__ __forceinline__ void lora_copy_row(const T* y, T* o, int j0, int j1, 
   }
   for (int j = j0 + lane; j < j1; j += 32)
     reinterpret_cast<unsigned short*>(o)[j] =
-        y != nullptr ? reinterpret_cast<const unsigned short*>(y)[j] : (unsigned short)0;
+        y != nullptr ? __ldcg(reinterpret_cast<const unsigned short*>(y) + j) : (unsigned short)0;
 }
 
 // Rows without an adapter: out = Y (0 without Y) unless they are the same, V = 0, over
