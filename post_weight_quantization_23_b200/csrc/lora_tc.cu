@@ -25,8 +25,8 @@
 // one ring of stages feeds both products, step 1 of the next piece runs ahead of step
 // 3 of this one, and the exchange has warps of its own (up to rank 64; rank 128
 // leaves no shared memory for the second operand and takes the steps in turn).
-// Warps: 0 TMA, 1 MMA, 2..5 exchange, 6..13 epilogue (two groups of four, tile by tile
-// in turn).  Every wait is bounded; a cluster in which one gives up drains its copies
+// Warps: 0 TMA, 1 MMA, 2..5 exchange, 6..17 epilogue (three groups of four, tile by tile
+// in turn, a TMEM buffer each).  Every wait is bounded; a cluster in which one gives up drains its copies
 // and MMAs, frees TMEM and writes NaN over its part of out and V.
 #include "lora.cuh"
 #include "tc_ptx.cuh"
@@ -38,10 +38,11 @@ namespace gptq {
 namespace {
 
 constexpr int LT_M = 128, LT_K = 64, LT_N = 64;
-constexpr int LT_XCH = 4, LT_EPI = 8;           // exchange and epilogue warps
+constexpr int LT_XCH = 4, LT_GROUPS = 3;        // exchange warps, epilogue groups of four
+constexpr int LT_EPI = 4 * LT_GROUPS;
 constexpr int LT_THREADS = 64 + 32 * (LT_XCH + LT_EPI);
 constexpr int LT_TILE = LT_M * LT_K * 2;        // 16 KB of X or Y
-constexpr int LT_TMEM = 512;                    // D1: 2 x 128 columns, D2: 4 x 64 from 256
+constexpr int LT_TMEM = 512;                    // D1: 2 x 128 columns, D2: a group each 64 from 256
 constexpr int LT_TABLE = 32;                    // pieces of a cluster looked up at a time
 
 template <int RP>
@@ -95,9 +96,9 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;  // copies that the producer started
   int* scan = (int*)(tmem_slot + 3);      // LT_THREADS / 32 + 1 ints
-  LoraPiece* table = (LoraPiece*)(scan + 16);
+  LoraPiece* table = (LoraPiece*)(scan + 20);
   float* rowback = (float*)(table + LT_TABLE);  // f16: [2][128] factors to take back
-  static_assert((3 * S + 18) * 8 + 12 + 64 + LT_TABLE * sizeof(LoraPiece) + 1024 <= 2304, "fits");
+  static_assert((3 * S + 18) * 8 + 12 + 80 + LT_TABLE * sizeof(LoraPiece) + 1024 <= 2304, "fits");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)cluster_rank();
@@ -116,7 +117,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     tc::mbar_init(v_full, LT_XCH);
     tc::mbar_init(v_empty, 1);
     tc::mbar_init(p_seen, LT_EPI);
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < LT_GROUPS; ++b) {
       tc::mbar_init(&d2_full[b], 1);
       tc::mbar_init(&d2_empty[b], 4);
     }
@@ -269,10 +270,10 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           ok = ok && tc::mbar_wait(v_full, (uint32_t)pi & 1u, abort_flag, a.spin);
           tc::tc_fence_after();
           for (int i = 0; i < nt && ok; ++i, ++g) {
-            const int b = g & 3;
+            const int b = g % LT_GROUPS;
             const uint32_t d2 = tmem + 256 + 64 * b;
-            if (g >= 4)
-              ok = tc::mbar_wait(&d2_empty[b], (uint32_t)(g / 4 - 1) & 1u, abort_flag, a.spin);
+            if (g >= LT_GROUPS)
+              ok = tc::mbar_wait(&d2_empty[b], (uint32_t)(g / LT_GROUPS - 1) & 1u, abort_flag, a.spin);
             ok = ok && tc::mbar_wait(&full[s], ph, abort_flag, a.spin);
             if (!ok) break;
             tc::tc_fence_after();
@@ -410,7 +411,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       if (lane < CS && *abort_flag)
         cluster_st_u32(cluster_map(tc::smem_u32((const void*)abort_flag), (uint32_t)lane), 1u);
     } else {
-      // ---- epilogue: group `grp` takes every second output tile ----
+      // ---- epilogue: group `grp` takes every third output tile ----
       const int grp = (warp - 2 - LT_XCH) / 4;
       const int quarter = warp & 3, row = quarter * 32 + lane;
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -430,10 +431,10 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         const int it0 = first_tile(i, n), g0 = base_g + nt * i;
         for (int q = 0; q < nt; ++q) {
           const int g = g0 + q, it = it0 + q;
-          if ((g & 1) != grp) continue;
-          const int s = it % S, b = g & 3;
+          if (g % LT_GROUPS != grp) continue;
+          const int s = it % S, b = grp;
           const int j0 = (rank + CS * q) * LT_N;
-          ok = tc::mbar_wait_warp(&d2_full[b], (uint32_t)(g / 4) & 1u, abort_flag, a.spin);
+          ok = tc::mbar_wait_warp(&d2_full[b], (uint32_t)(g / LT_GROUPS) & 1u, abort_flag, a.spin);
           if (!ok) break;
           // the MMA waited for the slot's copies, so this phase is over; the wait makes the
           // tile of Y visible here.  (Before the MMA the slot might still be a phase behind,
