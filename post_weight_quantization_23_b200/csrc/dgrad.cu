@@ -22,10 +22,12 @@
 //                16 bytes per word;
 //   warp 1       kind::f16 MMAs D[128 x N] += W^T dY^T per 128 columns, fp32 in TMEM.
 // The same warps are the epilogue (TMEM lane = column, TMEM column = token).
-// MT = 2 halves the stages' dY traffic and the launch picks N (launch_shape).
+// MT = 2 halves the stages' dY traffic, and where the tiles leave SMs idle the CTAs of a
+// cluster share a tile's rows of W (every split-th stage each) and add up through
+// distributed shared memory in a fixed order; launch_shape picks MT, N and the split.
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs, frees TMEM and
 // writes NaN over its outputs.
-#include "common.cuh"
+#include "cluster.cuh"
 #include "tc_ptx.cuh"
 
 #include <algorithm>
@@ -116,6 +118,7 @@ dgrad_general_kernel(const T* __restrict__ dY, int64_t lddy, int m, int n,
 constexpr int DT_K = 64;                    // rows of W per stage
 constexpr int DT_GROUP = 4;                 // warps of a dequantizing group
 constexpr int DT_NMAX = 256;
+constexpr int DT_LD = 132;                  // floats of a token's row of staged sums
 
 template <int MT>
 struct DtShape {
@@ -138,6 +141,7 @@ struct DtArgs {
   int64_t lddx;
   int n, m, k, G, ngroups;
   int N;          // tokens of a tile
+  int split;      // CTAs that share a tile (MT = 1)
   uint32_t spin;  // polls before a pipeline wait gives up
 };
 
@@ -163,7 +167,7 @@ template <> struct DtType<true> {
   __device__ static float back(T2 v) { return __low2float(v); }
 };
 
-template <bool BF16, int MT>
+template <bool BF16, int MT, bool SPLIT>
 __global__ void __launch_bounds__(DtShape<MT>::THREADS, 1)
 dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap pmap,
                 DtArgs a) {
@@ -183,8 +187,11 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
   volatile int* issued = abort_flag + 1;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int c0 = blockIdx.x * (MT * 128), t0 = blockIdx.y * a.N;
-  const int ns = (a.n + DT_K - 1) / DT_K;
+  const int split = SPLIT ? a.split : 1, part = SPLIT ? (int)blockIdx.x % split : 0;
+  const int c0 = (int)blockIdx.x / split * (MT * 128), t0 = blockIdx.y * a.N;
+  // stages of this CTA: part, part + split, ..
+  const int ns = ((a.n + DT_K - 1) / DT_K - part + split - 1) / split;
+  auto first_row = [&](int it) { return (part + it * split) * DT_K; };
   auto stage = [&](int it) { return dt_smem + (size_t)(it % S) * Sh::STAGE; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -199,14 +206,9 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
     tc::prefetch_tensormap(&ymap);
     tc::prefetch_tensormap(&pmap);
   }
-  // Only dY comes from the kernel before, and only dX may still be read by it: the copies
-  // of dY and the stores wait for it, the grids are requested at once (the packed weights
-  // must not be written by a kernel that lets this one start early).
+  pdl_wait();
   pdl_trigger();
-  if (warp == 1) {
-    pdl_wait();  // its CTAs have given their TMEM back
-    tc::tmem_alloc(tmem_slot, MT * 256);
-  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, MT * 256);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -215,15 +217,14 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
   if (warp == 0) {
     if (lane == 0) {
       const uint32_t bytes = Sh::P + (uint32_t)a.N * DT_K * 2;
-      pdl_wait();
       for (int it = 0; it < ns; ++it) {
         const int s = it % S;
         if (it >= S && !tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, a.spin))
           break;
         uint8_t* sb = stage(it);
         tc::mbar_arrive_expect_tx(&full[s], bytes);
-        tc::tma_load_2d(sb + Sh::A + Sh::B, &pmap, &full[s], c0 / 8, it * DT_K);
-        tc::tma_load_2d(sb + Sh::A, &ymap, &full[s], it * DT_K, t0);
+        tc::tma_load_2d(sb + Sh::A + Sh::B, &pmap, &full[s], c0 / 8, first_row(it));
+        tc::tma_load_2d(sb + Sh::A, &ymap, &full[s], first_row(it), t0);
         *issued = it + 1;
       }
     }
@@ -268,7 +269,7 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
     float fs[R];
     int fz[R];
     auto fetch = [&](int it) {
-      const int j = it * DT_K + grow;
+      const int j = first_row(it) + grow;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const bool ok = ghalf + 2 * i < ng && it < ns && j < a.n;
@@ -338,38 +339,70 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&ready[s]);
     }
+  }
+  // (the barrier first: the idle lanes of the copying and the issuing warp, polling beside
+  // their one busy lane, slowed the kernel by a seventh)
+  __syncthreads();
+  // all MMAs done (shared memory is free for the sums), all copies landed
+  const bool finished = tc::mbar_wait_warp(done, 0, abort_flag, tc::kSpinLimit);
+  if (*abort_flag && threadIdx.x == 0)
+    for (int p = max(0, *issued - S); p < *issued; ++p)
+      for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
+        if (tc::mbar_try_wait(&full[p % S], (uint32_t)(p / S) & 1u)) break;
+  __syncthreads();
+  tc::tc_fence_after();
+  const bool ok = finished && !*abort_flag;
+  float* sums = (float*)dt_smem;  // [N][DT_LD], split > 1
+  if (warp >= 2) {
     // epilogue: this warp's lane quarter of the 128-column tiles, its share of the tokens
-    const bool ok = tc::mbar_wait_warp(done, 0, abort_flag, a.spin) && !*abort_flag;
-    tc::tc_fence_after();
-    pdl_wait();
     const int quarter = warp & 3, nch = (a.N + 31) / 32;  // 32-token chunks of a tile
-    for (int x = grp; x < MT * nch; x += S) {
+    for (int x = (warp - 2) / 4; x < MT * nch; x += S) {
       const int mt = x / nch, q = x % nch * 32;
       const int c = c0 + mt * 128 + quarter * 32 + lane;
       typename Ty::T* out = reinterpret_cast<typename Ty::T*>(a.dX) + c;
       float v[32];
       tc::tmem_ld_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(256 * mt + q), v);
       tc::tmem_ld_wait();
+      if (!SPLIT) {
 #pragma unroll
-      for (int t = 0; t < 32; ++t)
-        if (c < a.k && q + t < a.N && t0 + q + t < a.m)
-          out[(int64_t)(t0 + q + t) * a.lddx] =
-              dg_out<typename Ty::T>(ok ? v[t] : __int_as_float(0x7fc00000));
+        for (int t = 0; t < 32; ++t)
+          if (c < a.k && q + t < a.N && t0 + q + t < a.m)
+            out[(int64_t)(t0 + q + t) * a.lddx] =
+                dg_out<typename Ty::T>(ok ? v[t] : __int_as_float(0x7fc00000));
+      } else {
+#pragma unroll
+        for (int t = 0; t < 32; ++t)
+          if (q + t < a.N)
+            sums[(q + t) * DT_LD + quarter * 32 + lane] = ok ? v[t] : __int_as_float(0x7fc00000);
+      }
     }
-  }
-  __syncthreads();
-  if (*abort_flag) {  // the copies and MMAs in flight end before shared memory and TMEM go
-    if (threadIdx.x == 0)
-      for (int p = max(0, *issued - S); p < *issued; ++p)
-        for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
-          if (tc::mbar_try_wait(&full[p % S], (uint32_t)(p / S) & 1u)) break;
-    if (threadIdx.x == 32)
-      for (uint32_t i = 0; i < tc::kSpinLimit; ++i)
-        if (tc::mbar_try_wait(done, 0)) break;
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  if (SPLIT) {
+    cluster_arrive();
+    cluster_wait();
+    // this CTA's share of the tokens, summed over the cluster
+    const int per = (a.N + split - 1) / split;
+    for (int e = threadIdx.x; e < per * 32; e += Sh::THREADS) {
+      const int t = part * per + e / 32, c4 = e % 32;
+      if (t >= a.N || t0 + t >= a.m) continue;
+      const uint32_t at = tc::smem_u32(sums + t * DT_LD + 4 * c4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < split; ++q) {
+        const float4 w = cluster_ld_f4(cluster_map(at, (uint32_t)q));
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+      }
+      const float f[4] = {v.x, v.y, v.z, v.w};
+      typename Ty::T* out = reinterpret_cast<typename Ty::T*>(a.dX) + (int64_t)(t0 + t) * a.lddx;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + 4 * c4 + i < a.k) out[c0 + 4 * c4 + i] = dg_out<typename Ty::T>(f[i]);
+    }
+    cluster_arrive();  // no CTA leaves while another reads its sums
+    cluster_wait();
+  }
   if (warp == 1) tc::tmem_dealloc(tmem, MT * 256);
 }
 
@@ -385,18 +418,23 @@ bool dgrad_tc_supported(const void* dY, int64_t lddy, const int32_t* qw, int bit
 // 16384) read and written, operands MT (16384 + N 128) read by the MMAs.  Measured
 // (22016 x 4096, 4096 tokens): 2 x 128 columns with 240 tokens 659 us, 256 tokens 678,
 // 128 columns with 240 tokens 746.
-void launch_shape(int64_t m, int64_t k, int& MT, int& N) {
-  const int sms = sm_count();
+// The join of a split tile is counted as 8000 + 24 N cycles.
+void launch_shape(int64_t m, int64_t n, int64_t k, int& MT, int& N, int& split) {
+  const int64_t sms = sm_count(), ns = cdiv(n, DT_K);
   int64_t best = 0;
   for (int mt = 1; mt <= 2; ++mt)
     for (int nn = 16; nn <= DT_NMAX; nn += 16) {
       const int64_t tiles = cdiv(k, mt * 128) * cdiv(m, nn);
-      const int64_t cost = cdiv(tiles, sms) * std::max(2 * mt * nn, nn * (1 + mt) + 320 * mt);
-      if (best == 0 || cost < best) best = cost, MT = mt, N = nn;
+      const int64_t stage = std::max(2 * mt * nn, nn * (1 + mt) + 320 * mt);
+      for (int sp = 1; sp <= (mt == 1 ? 8 : 1) && sp * 4 <= std::max<int64_t>(ns, 4); sp *= 2) {
+        if (sp > 1 && tiles * sp > sms) break;
+        const int64_t cost = cdiv(tiles * sp, sms) * cdiv(ns, sp) * stage + (sp > 1 ? 8000 + 24 * nn : 0);
+        if (best == 0 || cost < best) best = cost, MT = mt, N = nn, split = sp;
+      }
     }
 }
 
-template <bool BF16, int MT>
+template <bool BF16, int MT, bool SPLIT>
 gptq_status launch_dgrad(const void* dY, int64_t lddy, const int32_t* qw, DtArgs a, cudaStream_t s) {
   using Sh = DtShape<MT>;
   EncodeTiledFn enc = tensormap_encoder();
@@ -422,11 +460,15 @@ gptq_status launch_dgrad(const void* dY, int64_t lddy, const int32_t* qw, DtArgs
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return GPTQ_ERR_CUDA;
   }
-  if (smem_optin((const void*)dgrad_tc_kernel<BF16, MT>, Sh::SMEM) != cudaSuccess)
+  if (smem_optin((const void*)dgrad_tc_kernel<BF16, MT, SPLIT>, Sh::SMEM) != cudaSuccess)
     return GPTQ_ERR_CUDA;
-  launch_pdl(dgrad_tc_kernel<BF16, MT>,
-             dim3((unsigned)cdiv(a.k, MT * 128), (unsigned)cdiv(a.m, a.N)), dim3(Sh::THREADS),
-             Sh::SMEM, s, ymap, pmap, a);
+  static_assert(MT == 2 || DT_NMAX * DT_LD * 4 <= Sh::S * Sh::STAGE, "a split tile's sums fit");
+  const dim3 grid((unsigned)(cdiv(a.k, MT * 128) * a.split), (unsigned)cdiv(a.m, a.N));
+  if (!SPLIT)
+    launch_pdl(dgrad_tc_kernel<BF16, MT, SPLIT>, grid, dim3(Sh::THREADS), Sh::SMEM, s, ymap, pmap, a);
+  else
+    launch_cluster_pdl(dgrad_tc_kernel<BF16, MT, SPLIT>, grid, dim3(Sh::THREADS), Sh::SMEM, a.split, s, ymap,
+                       pmap, a);
   GPTQ_CHECK_LAUNCH();
   return GPTQ_OK;
 }
@@ -444,12 +486,14 @@ gptq_status dgrad_impl(const void* dY, gptq_dtype dt, int64_t m, int64_t n, int6
     a.n = (int)n, a.m = (int)m, a.k = (int)k, a.G = G, a.ngroups = (int)ngroups;
     a.spin = wait_limit();
     int MT = 1;
-    launch_shape(m, k, MT, a.N);
+    launch_shape(m, n, k, MT, a.N, a.split);
     if (dt == GPTQ_BF16)
-      return MT == 2 ? launch_dgrad<true, 2>(dY, lddy, qw, a, s)
-                     : launch_dgrad<true, 1>(dY, lddy, qw, a, s);
-    return MT == 2 ? launch_dgrad<false, 2>(dY, lddy, qw, a, s)
-                   : launch_dgrad<false, 1>(dY, lddy, qw, a, s);
+      return MT == 2       ? launch_dgrad<true, 2, false>(dY, lddy, qw, a, s)
+             : a.split > 1 ? launch_dgrad<true, 1, true>(dY, lddy, qw, a, s)
+                           : launch_dgrad<true, 1, false>(dY, lddy, qw, a, s);
+    return MT == 2       ? launch_dgrad<false, 2, false>(dY, lddy, qw, a, s)
+           : a.split > 1 ? launch_dgrad<false, 1, true>(dY, lddy, qw, a, s)
+                         : launch_dgrad<false, 1, false>(dY, lddy, qw, a, s);
   }
   const dim3 grid((unsigned)cdiv(k, DG_C), (unsigned)cdiv(m, DG_T));
   if (dt == GPTQ_F16)

@@ -17,8 +17,8 @@
 //      fixed order, scales, and hands V to all.  V as hi + lo of the 16-bit type
 //      (f16: each row scaled by a power of two, taken back exactly) becomes the A
 //      operand of
-//   3. CTA q takes every CS-th 64-column tile of the output, D2[128 x 64] in four
-//      TMEM buffers; the tile of Y arrives by TMA beside Q, the sum is rounded once
+//   3. CTA q takes every CS-th 64-column tile of the output, D2[128 x 64] in a TMEM
+//      buffer per epilogue group; the tile of Y arrives by TMA beside Q, the sum is rounded once
 //      and stored row by row (a TMA store would also write rows of the next request).
 // A CTA has an SM to itself (every kernel that uses tcgen05 gets one CTA per SM on
 // this driver, whatever its registers and shared memory), so the overlap is inside:
