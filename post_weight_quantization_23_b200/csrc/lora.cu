@@ -191,6 +191,9 @@ __device__ __forceinline__ int ld_piece(const LdWindow& w, int p, LdShared& sm) 
 //      first scaled by a power of two, so that neither leaves the type's range).
 // Latency is what it spends its time on, so the tiles of B and Y are requested several at a
 // time, the first of them before the barrier.  One launch, no workspace, sums in a fixed order.
+// One token, rank 16, 4096 -> 4096: 4.9 us (look-up 1.2, loads of A 1.0, sums and exchange
+// 1.2, output 0.6; the rest launch); 64 tokens over 16 adapters, 4096 -> 12288: 11.7 us
+// (a piece per token, each adapter read four times: 14.4).
 template <bool BF16, int RP>
 __global__ void __launch_bounds__(LD_THREADS, RP <= 32 ? 3 : RP == 64 ? 2 : 1)
 lora_decode_kernel(LoraArgs a, int yvec, int late) {
@@ -473,7 +476,8 @@ gptq_status lora_general(const LoraArgs& a, bool bf16, bool backward, cudaStream
 }  // namespace
 
 // Batches of up to this many rows go to the decode kernel whole; in larger ones it
-// takes the requests of up to LORA_SHORT rows.
+// takes the requests of up to LORA_SHORT rows.  (A tensor-core piece costs its 128 rows
+// whatever it holds, 10 us and more through the exchange; three pieces of 8 rows less.)
 constexpr int LORA_DECODE_ROWS = 256;
 constexpr int LORA_SHORT = 24;
 

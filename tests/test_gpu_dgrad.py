@@ -37,6 +37,11 @@ CASES = [
     (70, 512, 8, 32, 129, BF, False, False),
     (80, 1024, 4, 128, 90, BF, True, True),        # act-order groups
     (48, 512, 4, 128, 20, H, True, False),
+    # few tiles: the rows of W split over a cluster of 2, 4 or 8
+    (2200, 1024, 4, 128, 1, H, False, False),
+    (4104, 128, 4, -1, 200, BF, False, False),
+    (520, 384, 4, 32, 90, BF, False, False),
+    (1000, 2048, 4, 64, 250, H, False, False),
 ]
 
 
