@@ -27,6 +27,8 @@
 // distributed shared memory in a fixed order; launch_shape picks MT, N and the split.
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs, frees TMEM and
 // writes NaN over its outputs.
+// 22016 x 4096, 4096 tokens: 600 us, 1230 TFLOP/s, 0.72 of the measured bf16 burst (690 us
+// in a long run, under the power cap); 4096 x 4096, 512 tokens: 29 us.
 #include "cluster.cuh"
 #include "tc_ptx.cuh"
 

@@ -26,6 +26,9 @@
 // which are the epilogue too.  The number of stages is a multiple of the groups, so a
 // slot belongs to one group, which sees every phase of its barrier (a wait that skips
 // phases cannot tell the one before from the one it wants).  Every wait is bounded; a CTA that gives up writes NaN.
+// 4096 tokens, rank 64, 4096 x 11008 from codes: 51 us.  A CTA of the code columns takes 1000
+// cycles per 64-token tile (conversion of codes and W, some 2000 warp instructions), one of
+// the bf16 columns 700 to 900 (copies' latency); at HBM's rate the kernel's 108 MB take 17 us.
 #include "lora.cuh"
 #include "tc_ptx.cuh"
 
