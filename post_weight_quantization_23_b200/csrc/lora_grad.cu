@@ -14,8 +14,8 @@
 //     gradients are small, f16 would lose them among its subnormals), side by side as one
 //     operand of 2 RP columns: S is read from shared memory, whose bandwidth sets the
 //     pace, once for both, and the two halves of D are added at the end.
-//   S in bf16 is used as it is.  S in f16 is split into two bf16 parts as well (exact but
-//     for f16's smallest subnormals), three products, lo x lo left out.
+//   S in bf16 is used as it is.  S in f16 is split into two bf16 parts as well (exactly),
+//     three products, lo x lo left out.
 //   S in 8-bit codes becomes bf16 exactly (|code| <= 127), and its scales, one per token
 //     and 128-column block, multiply the rows of W: the checkpoint is never restored.
 // Tiles to be converted land in a ring of their own, deeper than the operands' (a tile of
@@ -25,7 +25,8 @@
 // Warps: 0 TMA, 1 MMA, then the operand warps (groups of four, tile by tile in turn),
 // which are the epilogue too.  The number of stages is a multiple of the groups, so a
 // slot belongs to one group, which sees every phase of its barrier (a wait that skips
-// phases cannot tell the one before from the one it wants).  Every wait is bounded; a CTA that gives up writes NaN.
+// phases cannot tell the one before from the one it wants).
+// Every wait is bounded; a CTA that gives up writes NaN.
 // 4096 tokens, rank 64, 4096 x 11008 from codes: 51 us.  A CTA of the code columns takes 1000
 // cycles per 64-token tile (conversion of codes and W, some 2000 warp instructions), one of
 // the bf16 columns 700 to 900 (copies' latency); at HBM's rate the kernel's 108 MB take 17 us.
