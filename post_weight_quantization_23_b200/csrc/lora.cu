@@ -192,17 +192,18 @@ __device__ __forceinline__ int ld_piece(const LdWindow& w, int p, LdShared& sm) 
 // Latency is what it spends its time on, so the tiles of B and Y are requested several at a
 // time, the first of them before the barrier.  One launch, no workspace, sums in a fixed order.
 // One token, rank 16, 4096 -> 4096: 4.9 us (look-up 1.2, loads of A 1.0, sums and exchange
-// 1.2, output 0.6; the rest launch); 64 tokens over 16 adapters, 4096 -> 12288: 11.7 us
-// (a piece per token, each adapter read four times: 14.4).
+// 1.2, output 0.6; the rest launch); 64 tokens over 16 adapters, 4096 -> 12288: 10.0 us
+// (a piece per token, each adapter read four times: 14.4; three CTAs an SM, with fewer tiles
+// of B in flight and more clusters that find no piece: 11.7).
 template <bool BF16, int RP>
-__global__ void __launch_bounds__(LD_THREADS, RP <= 32 ? 3 : RP == 64 ? 2 : 1)
+__global__ void __launch_bounds__(LD_THREADS, RP <= 64 ? 2 : 1)
 lora_decode_kernel(LoraArgs a, int yvec, int late) {
   using Ty = LoraType<BF16>;
   using T = typename Ty::T;
   constexpr int MT = RP / 16;                  // 16-row tiles of the rank
   constexpr int KC = RP >= 32 ? RP / 32 : 1;   // 32-wide chunks of the rank in product 2
   constexpr int NS = RP >= 32 ? 2 : 1;         // 16-wide steps per chunk
-  constexpr int U = RP == 16 ? 4 : RP <= 64 ? 2 : 1;  // tiles of B in flight
+  constexpr int U = RP == 16 ? 6 : RP == 32 ? 4 : RP == 64 ? 2 : 1;  // tiles of B in flight
   extern __shared__ __align__(16) float ld_smem[];
   constexpr int PS = RP * LD_TT;               // values of one partial sum
   float* red = ld_smem;                        // [LD_WARPS][PS] per-warp sums, then V
@@ -496,8 +497,10 @@ gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
     a.min_len = 1;
     a.max_len = LORA_SHORT;
   }
+  // a piece that is not full is the last of its adapter (or of none) in its window
+  const int64_t last = cdiv(a.nreq, LD_THREADS) * std::min(a.na + 1, LD_THREADS);
   const int64_t pieces =
-      std::min<int64_t>(std::min<int64_t>(a.m, (int64_t)a.m / LD_TT + a.nreq),
+      std::min<int64_t>(std::min<int64_t>(a.m, (int64_t)a.m / LD_TT + std::min<int64_t>(a.nreq, last)),
                         a.nreq * cdiv(std::min(a.max_len, a.m), LD_TT));
   return bf16 ? decode_ranks<true>(a, pieces, tc, s) : decode_ranks<false>(a, pieces, tc, s);
 }
