@@ -13,7 +13,7 @@
 //      whole runs of a row): TMA brings 128 x 64 tiles of X and P, one thread
 //      issues kind::f16 MMAs D1[128 x RP] into TMEM.
 //   2. Exchange through distributed shared memory: each CTA hands its partial sums
-//      to the CTA that owns the row (128 / CS rows each); the owner adds them in a
+//      to the CTA that owns the row (128 / CS rows each, in eights); the owner adds them in a
 //      fixed order, scales, and hands V to all.  V as hi + lo of the 16-bit type
 //      (f16: each row scaled by a power of two, taken back exactly) becomes the A
 //      operand of
@@ -50,15 +50,18 @@ constexpr int LT_TILE = LT_M * LT_K * 2;        // 16 KB of X or Y
 constexpr int LT_TMEM = 512;                    // D1: 2 x 128 columns, D2: a group each 64 from 256
 constexpr int LT_TABLE = 32;                    // pieces of a cluster looked up at a time
 
-template <int RP>
+template <int RP, int CS>
 struct LtShape {
+  // rows whose sums a CTA forms, in whole swizzle periods: the last owner may have fewer
+  static constexpr int OWNED = (LT_M / 8 + CS - 1) / CS * 8;
   static constexpr bool PIPE = RP <= 64;                // step 1 runs a piece ahead
   static constexpr int PQ = (RP > 64 ? RP : 64) * 128;  // bytes of a P or Q tile
   static constexpr int STAGE = LT_TILE + PQ;
   static constexpr int OPND = (RP > 32 ? RP : 32) * 512;  // V as hi | lo, 64-column atoms
   static constexpr int VBUF = RP * 512;                  // fp32, 128 rows
-  static constexpr int RED = PIPE ? VBUF : 0;            // else in the operand's place
-  static constexpr int S = RP == 16 ? 8 : RP == 32 ? 7 : RP == 64 ? 5 : 3;
+  static constexpr int RED = PIPE ? CS * OWNED * RP * 4 : 0;  // else in the operand's place
+  static_assert(PIPE || CS * OWNED * RP * 4 <= OPND, "fits");
+  static constexpr int S = RP == 16 ? (RED > VBUF ? 7 : 8) : RP == 32 ? 7 : RP == 64 ? 5 : 3;
   static constexpr size_t SMEM = (size_t)S * STAGE + OPND + VBUF + RED + 2304;
 };
 
@@ -75,9 +78,9 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                LoraArgs a, int ovec) {
   using Ty = LoraType<BF16>;
   using T = typename Ty::T;
-  using Sh = LtShape<RP>;
+  using Sh = LtShape<RP, CS>;
   constexpr int S = Sh::S;
-  constexpr int OWNED = LT_M / CS;              // rows whose sums a CTA forms
+  constexpr int OWNED = Sh::OWNED;
   constexpr int OWN4 = OWNED * RP / 4;          // their float4s
   extern __shared__ __align__(1024) uint8_t lt_smem[];  // the swizzle atoms need 1024
   uint8_t* opnd = lt_smem + S * Sh::STAGE;
@@ -341,7 +344,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           // each owner's rows to it, consecutive lanes to consecutive addresses
           const uint32_t dst = tc::smem_u32(red) + 16u * (uint32_t)(rank * OWN4);
 #pragma unroll 4
-          for (int e = xt; e < CS * OWN4; e += 32 * LT_XCH)
+          for (int e = xt; e < LT_M * RP / 4; e += 32 * LT_XCH)
             cluster_st_f4(cluster_map(dst + 16u * (uint32_t)(e % OWN4), (uint32_t)(e / OWN4)),
                           reinterpret_cast<const float4*>(vbuf)[e]);
           __syncwarp();
@@ -353,7 +356,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           // V over the block of vbuf that went to it, which has arrived there by now.)
           const float sc = a.scaling[pc.a];
           const float4* part = reinterpret_cast<const float4*>(red);
-          for (int e = xt; e < OWN4; e += 32 * LT_XCH) {
+          for (int e = xt; e < min(OWN4, LT_M * RP / 4 - rank * OWN4); e += 32 * LT_XCH) {
             float4 v = part[e];
 #pragma unroll
             for (int c = 1; c < CS; ++c) {
@@ -574,9 +577,19 @@ bool lt_map(CUtensorMap* map, bool bf16, int dims, const void* p, int64_t d0, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters that are resident at once (0: the shared memory is refused).
+template <bool BF16, int RP, bool BWD, int CS>
+int tc_fit() {
+  if (smem_optin((const void*)lora_tc_kernel<BF16, RP, BWD, CS>, LtShape<RP, CS>::SMEM) != cudaSuccess)
+    return 0;
+  return resident_clusters((const void*)lora_tc_kernel<BF16, RP, BWD, CS>, CS, LT_THREADS,
+                           LtShape<RP, CS>::SMEM);
+}
+
+
 template <bool BF16, int RP, bool BWD, int CS>
 gptq_status launch_tc(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
-  using Sh = LtShape<RP>;
+  using Sh = LtShape<RP, CS>;
   static_assert(Sh::SMEM <= 232448, "shared memory of a CTA");
   CUtensorMap xm, pm, qm, ym;
   const int64_t r = a.r, K = a.K, N = a.N, na = a.na;
@@ -591,12 +604,11 @@ gptq_status launch_tc(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
     ok = ok && lt_map(&ym, BF16, 2, a.Y, N, a.m, 1, a.ldy, 0, LT_M);
   else
     ym = xm;  // not read
-  if (!ok || smem_optin((const void*)lora_tc_kernel<BF16, RP, BWD, CS>, Sh::SMEM) != cudaSuccess)
-    return GPTQ_ERR_CUDA;
+  if (!ok) return GPTQ_ERR_CUDA;
   const int ovec = (uintptr_t)a.out % 16 == 0 && a.ldo % 8 == 0;
   // as many clusters as fit the device at once; each takes piece after piece
-  const int fit = resident_clusters((const void*)lora_tc_kernel<BF16, RP, BWD, CS>, CS, LT_THREADS,
-                                    Sh::SMEM);
+  const int fit = tc_fit<BF16, RP, BWD, CS>();
+  if (fit == 0) return GPTQ_ERR_CUDA;
   pieces = std::min<int64_t>(pieces, fit);
   launch_cluster_pdl(lora_tc_kernel<BF16, RP, BWD, CS>, dim3((unsigned)(pieces * CS)),
                      dim3(LT_THREADS), Sh::SMEM, CS, s, xm, pm, qm, ym, a, ovec);
@@ -604,12 +616,38 @@ gptq_status launch_tc(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
   return GPTQ_OK;
 }
 
-// Clusters of 8 where all pieces fit the device at once that way, else of 4 (more of
-// the 148 SMs are reached: 33 clusters of 4 fit, 15 of 8).
+// The size of the clusters.  A piece takes a cluster the longer the fewer CTAs it has, but
+// larger clusters fit the device less often (the GPCs' 16 to 18 free SMs: 15 of 8, 22 of 6,
+// 26 of 5, 33 of 4, 45 of 3): the size whose rounds over the pieces, by its CTAs, are fewest.
+// Measured (4096 -> 11008, rank 64), clusters of 8, 6, 4, 3: 600 tokens 28, 33, 42, 51 us;
+// 2000 tokens 48, 38, 45, 53; 5000 tokens 72, 66, 82, 64; 8192 tokens 110, 94, 93, 105.
+// The lengths are on the device.  Of several requests one in 512 rows is taken to be long,
+// with a last piece half full, and the others to be single rows; a wrong guess costs time.
 template <bool BF16, int RP, bool BWD>
 gptq_status tc_cluster(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
-  if (pieces * 8 <= sm_count() * 4 / 5) return launch_tc<BF16, RP, BWD, 8>(a, pieces, s);
-  return launch_tc<BF16, RP, BWD, 4>(a, pieces, s);
+  const int64_t longer = std::min<int64_t>(a.nreq, std::max(1, a.m / 512));
+  const int64_t rows = a.m - (a.nreq - longer);
+  const int64_t guess =
+      a.nreq == 1 ? pieces : std::max<int64_t>(1, (rows + longer * (LT_M / 2)) / LT_M);
+  int size = 0;
+  int64_t rounds = 0;
+  auto weigh = [&](int cs, int fit) {
+    const int64_t n = fit > 0 ? cdiv(guess, fit) : INT32_MAX;
+    if (size == 0 || n * size < rounds * cs || (n * size == rounds * cs && n < rounds))
+      size = cs, rounds = n;
+  };
+  weigh(8, tc_fit<BF16, RP, BWD, 8>());
+  weigh(4, tc_fit<BF16, RP, BWD, 4>());
+  if constexpr (RP <= 64) {
+    weigh(6, tc_fit<BF16, RP, BWD, 6>());
+    weigh(5, tc_fit<BF16, RP, BWD, 5>());
+    weigh(3, tc_fit<BF16, RP, BWD, 3>());
+    if (size == 3) return launch_tc<BF16, RP, BWD, 3>(a, pieces, s);
+    if (size == 5) return launch_tc<BF16, RP, BWD, 5>(a, pieces, s);
+    if (size == 6) return launch_tc<BF16, RP, BWD, 6>(a, pieces, s);
+  }
+  if (size == 4) return launch_tc<BF16, RP, BWD, 4>(a, pieces, s);
+  return launch_tc<BF16, RP, BWD, 8>(a, pieces, s);
 }
 
 template <bool BF16, bool BWD>
