@@ -122,13 +122,18 @@ __device__ __forceinline__ int lora_find_pieces(const LoraRequests& a, int TT, i
   const int per = (a.nreq + NT - 1) / NT;
   const int q0 = min(a.nreq, tid * per), q1 = min(a.nreq, q0 + per);
   int own = 0;
-  auto pieces = [&](int q) {
-    const int ad = a.adapter[q];
-    return (only >= 0 ? ad != only : ad < 0 || ad >= a.na)
-               ? 0
-               : lora_pieces(a.starts, q, a.m, TT, a.min_len, a.max_len);
+  // the thread's first request; mostly its only one, and its three loads are in flight together
+  int b0 = 0, e0 = 0, ad0 = -1;
+  if (q0 < q1) b0 = a.starts[q0], e0 = a.starts[q0 + 1], ad0 = a.adapter[q0];
+  auto pieces = [&](int q, int& b, int& e, int& ad) {
+    b = lora_clamp(q == q0 ? b0 : a.starts[q], a.m);
+    e = lora_clamp(q == q0 ? e0 : a.starts[q + 1], a.m);
+    ad = q == q0 ? ad0 : a.adapter[q];
+    if (only >= 0 ? ad != only : ad < 0 || ad >= a.na) return 0;
+    return e - b < a.min_len || e - b > a.max_len ? 0 : (e - b + TT - 1) / TT;
   };
-  for (int q = q0; q < q1; ++q) own += pieces(q);
+  int b, e, ad;
+  for (int q = q0; q < q1; ++q) own += pieces(q, b, e, ad);
   int inc = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -145,23 +150,23 @@ __device__ __forceinline__ int lora_find_pieces(const LoraRequests& a, int TT, i
   }
   // the i-th entry is piece first + (skip + i) * stride
   const int64_t p0 = first + (int64_t)skip * stride;
-  const int64_t n = total > p0 ? min((int64_t)cap, (total - p0 + stride - 1) / stride) : 0;
-  for (int q = q0; q < q1; ++q) {
-    const int c = pieces(q);
+  const int n = total > p0 ? (int)min((uint32_t)cap, ((uint32_t)(total - p0) + stride - 1) / stride) : 0;
+  for (int q = q0; q < q1 && n > 0; ++q) {
+    const int c = pieces(q, b, e, ad);
     if (c > 0) {
-      int64_t i = at <= p0 ? 0 : (at - p0 + stride - 1) / stride;
-      for (; i < n && p0 + i * stride < at + c; ++i) {
+      uint32_t i = at <= p0 ? 0 : ((uint32_t)(at - p0) + stride - 1) / stride;
+      for (; i < (uint32_t)n && p0 + (int64_t)i * stride < at + c; ++i) {
         LoraPiece r;
-        r.t0 = lora_clamp(a.starts[q], a.m) + (int)(p0 + i * stride - at) * TT;
-        r.cnt = min(TT, lora_clamp(a.starts[q + 1], a.m) - r.t0);
-        r.a = a.adapter[q];
+        r.t0 = b + (int)(p0 + (int64_t)i * stride - at) * TT;
+        r.cnt = min(TT, e - r.t0);
+        r.a = ad;
         table[i] = r;
       }
     }
     at += c;
   }
   __syncthreads();
-  return (int)n;
+  return n;
 }
 
 // Columns [j0, j1) of a row from y (zeros if NULL) to o by one warp; eight vectors are

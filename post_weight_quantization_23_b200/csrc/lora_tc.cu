@@ -27,7 +27,7 @@
 // leaves no shared memory for the second operand and takes the steps in turn).
 // Warps: 0 TMA, 1 MMA, 2..5 exchange, 6..17 epilogue (three groups of four, tile by tile
 // in turn, a TMEM buffer each).
-// 8192 tokens, rank 64, 4096 -> 11008: 93 us (432 MB, 4.6 TB/s, 0.72 of measured HBM): its
+// 8192 tokens, rank 64, 4096 -> 11008: 89 us (432 MB, 4.8 TB/s, 0.75 of measured HBM): its
 // two rounds of output tiles run at 5.8 TB/s, the first reduction and exchange (22 us) before
 // them are half covered by the second reduction.  Two epilogue groups instead of three: 83
 // -> 87 us for 3001 ragged f16 tokens at rank 8; asking for tiles in L2 ahead changed nothing.
@@ -176,7 +176,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   for (int chunk = 0;; ++chunk) {
     int n = np;
     if (warp == 0) {
-      if (lane == 0) {
+      if (tc::elect_one()) {
         int it = base_it;
         bool ok = true;
         auto take = [&](uint32_t kind) {  // the next slot of the ring, empty; kind 1: output tile
@@ -317,6 +317,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         const int pi = base_p + i, b = pi & 1;
         const uint32_t ph = (uint32_t)pi & 1u;
         const LoraPiece pc = table[i];
+        const float sc = a.scaling[pc.a];
+        const int live4 = (pc.cnt + 7) / 8 * 8 * (RP / 4);  // float4s of the rows that are used
         bool ok = tc::mbar_wait_warp(&d1_full[b], (uint32_t)(pi / 2) & 1u, abort_flag, a.spin);
         if (ok) {  // this CTA's partial sums, to shared memory
           tc::tc_fence_after();
@@ -344,7 +346,7 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           // each owner's rows to it, consecutive lanes to consecutive addresses
           const uint32_t dst = tc::smem_u32(red) + 16u * (uint32_t)(rank * OWN4);
 #pragma unroll 4
-          for (int e = xt; e < LT_M * RP / 4; e += 32 * LT_XCH)
+          for (int e = xt; e < live4; e += 32 * LT_XCH)
             cluster_st_f4(cluster_map(dst + 16u * (uint32_t)(e % OWN4), (uint32_t)(e / OWN4)),
                           reinterpret_cast<const float4*>(vbuf)[e]);
           __syncwarp();
@@ -354,9 +356,8 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         if (ok) {
           // the rows that this CTA owns: add the parts, scale, hand V to all.  (A peer writes
           // V over the block of vbuf that went to it, which has arrived there by now.)
-          const float sc = a.scaling[pc.a];
           const float4* part = reinterpret_cast<const float4*>(red);
-          for (int e = xt; e < min(OWN4, LT_M * RP / 4 - rank * OWN4); e += 32 * LT_XCH) {
+          for (int e = xt; e < min(OWN4, live4 - rank * OWN4); e += 32 * LT_XCH) {
             float4 v = part[e];
 #pragma unroll
             for (int c = 1; c < CS; ++c) {
@@ -478,13 +479,17 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           tc::tc_fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&d2_empty[b]);
-          // this warp's 32 rows, 128 contiguous bytes per row; all reads before the first store
+          // this warp's 32 rows, 128 contiguous bytes per row; the slot goes back before the
+          // stores, whose way to L2 it would wait for
           const int c = lane % 8, j = j0 + 8 * c, r0 = quarter * 32 + lane / 8;
           uint4 w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             w[e] = *reinterpret_cast<const uint4*>(ys + (r0 + 4 * e) * 128 +
                                                    ((c ^ ((r0 + 4 * e) & 7)) << 4));
+          tc::fence_proxy_async_smem();  // the next copy into the slot comes after these accesses
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&empty2[s]);
           T* o = out + (int64_t)(pc.t0 + r0) * a.ldo + j;
           if (ovec && j + 8 <= a.N) {
 #pragma unroll
@@ -502,9 +507,6 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                       (unsigned short)(u[x / 2] >> (16 * (x % 2)));
             }
           }
-          tc::fence_proxy_async_smem();  // the next copy into the slot comes after these accesses
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&empty2[s]);
         }
       }
     }
