@@ -629,8 +629,8 @@ template <bool BF16, int RP, bool BWD>
 gptq_status tc_cluster(const LoraArgs& a, int64_t pieces, cudaStream_t s) {
   const int64_t longer = std::min<int64_t>(a.nreq, std::max(1, a.m / 512));
   const int64_t rows = a.m - (a.nreq - longer);
-  const int64_t guess =
-      a.nreq == 1 ? pieces : std::max<int64_t>(1, (rows + longer * (LT_M / 2)) / LT_M);
+  const int64_t guess = a.nreq == 1 ? cdiv(a.m, LT_M)
+                                    : std::max<int64_t>(1, (rows + longer * (LT_M / 2)) / LT_M);
   int size = 0;
   int64_t rounds = 0;
   auto weigh = [&](int cs, int fit) {

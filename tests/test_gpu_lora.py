@@ -494,3 +494,31 @@ def test_two_streams_at_once():
         _, _, want, y = ss[i % 2]
         for p, q in zip(o, want + (y,)):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype,r", [(BF, 64), (H, 32), (BF, 8), (H, 16)])
+@pytest.mark.parametrize("m", [1920, 2180, 3111, 4200, 5290])
+def test_cluster_sizes(dtype, r, m):
+    # as many pieces as make clusters of 8, 6, 5, 4 and 3 CTAs the choice; the last piece and
+    # the last owner's rows of it ragged; once one request, once three and rows of none
+    from post_weight_quantization_23_b200 import lora_add, lora_backward
+    k, n = 456, 328
+    for lens, ids, first, tail in (([m], [0], 0, 0), ([m - 533, 412, 121], [0, 2, 1], 2, 3)):
+        s = R.make(dtype, k, n, r, 2, lens, ids, m + r, first, tail)
+        ref, bound, Vr, bv, cov = R.add_ref(s, dtype)
+        V = torch.full((s["Y"].shape[0], r), 5.0, device="cuda")
+        out = torch.full_like(s["Y"], 7.0)
+        lora_add(s["Y"], s["X"], s["A"], s["B"], s["scaling"], s["starts"], s["adapter"], out=out,
+                 V=V)
+        R.check(out[cov], ref[cov], bound[cov], "out")
+        R.check(V[cov], Vr[cov], bv[cov], "V")
+        assert (out[~cov] == 7.0).all() and (V[~cov] == 5.0).all()
+        s["V"] = V
+        b = R.backward_ref(s, dtype, s["X"].to(R.D))
+        dX = torch.full_like(s["dX"], 7.0)
+        got = lora_backward(s["dY"], s["X"], V, s["A"], s["B"], s["scaling"], s["starts"],
+                            s["adapter"], s["dX"], out=dX)
+        R.check(dX[cov], b["out"][0][cov], b["out"][1][cov], "dX")
+        R.check(got[1], *b["dA"], "dA")
+        R.check(got[2], *b["dB"], "dB")
+        assert (dX[~cov] == 7.0).all()
