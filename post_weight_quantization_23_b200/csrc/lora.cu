@@ -479,7 +479,12 @@ gptq_status lora_general(const LoraArgs& a, bool bf16, bool backward, cudaStream
 // Batches of up to this many rows go to the decode kernel whole; in larger ones it
 // takes the requests of up to LORA_SHORT rows.  (A tensor-core piece costs its 128 rows
 // whatever it holds, 10 us and more through the exchange; three pieces of 8 rows less.)
-constexpr int LORA_DECODE_ROWS = 256;
+// The decode kernel's time grows with every 8 rows and with the rank, the other's hardly.
+// One request, decode against tensor cores: rank 16, 4096 -> 4096, 256 rows 7.6 and 15.1 us,
+// 768 rows 14.4 and 15.1; rank 32, 11008 -> 4096, 512 rows 17.8 and 18.5, 640 rows 22.7 and
+// 19.1; rank 64, 4096 -> 11008, 257 rows 17.1 and 25.4, 384 rows 27.4 and 25.3; rank 128,
+// 4096 -> 4096, 192 rows 19.9 and 23.7, 256 rows 27.4 and 23.8.
+constexpr int lora_decode_rows(int r) { return r <= 16 ? 704 : r <= 32 ? 512 : r <= 64 ? 256 : 192; }
 constexpr int LORA_SHORT = 24;
 
 gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
@@ -488,7 +493,7 @@ gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
   // the decode kernel reads rows of X, A and B in 16-byte pieces
   if (!rows16(a.X, a.ldx) || !rows16(a.P, a.K) || !rows16(a.Q, a.r))
     return lora_general(a, bf16, false, s);
-  const bool tc = a.m > LORA_DECODE_ROWS && lora_tc_supported(a, false);
+  const bool tc = a.m > lora_decode_rows(a.r) && lora_tc_supported(a, false);
   if (tc) {
     // the long requests first, the short ones beside them on the SMs that are left
     if (a.nreq > 1) a.min_len = LORA_SHORT + 1;

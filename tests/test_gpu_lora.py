@@ -522,3 +522,33 @@ def test_cluster_sizes(dtype, r, m):
         R.check(got[1], *b["dA"], "dA")
         R.check(got[2], *b["dB"], "dB")
         assert (dX[~cov] == 7.0).all()
+
+
+# the tests above again with batches long enough for the tensor-core kernel at every rank
+
+@pytest.mark.parametrize("case", [
+    (H, 512, 768, 16, 4, [300] + [1] * 40 + [33] * 9 + [257, 25, 24, 0, 140],
+     [i % 6 - 1 for i in range(55)], 4, 4),
+    (BF, 1024, 520, 32, 3, [0, 1, 129, 0, 500, 8, 7, 333], [0, 1, 2, 0, 1, 2, 0, 1], 3, 5),
+    (H, 136, 264, 8, 2, [127, 650, 2], [1, 0, 1], 1, 2),
+    (BF, 11008, 256, 16, 1, [800], [0], 0, 0),
+    (H, 8, 8, 8, 1, [777], [0], 0, 9),
+], ids=lambda c: f"r{c[3]}_m{sum(c[5])}")
+def test_add_long(case):
+    test_add(case)
+    test_add_without_y(case)
+
+
+@pytest.mark.parametrize("xoff,ypad", [(0, 8), (0, 3), (3, 5), (8, 0)])
+def test_add_long_strided(xoff, ypad):
+    test_add_strided(xoff, ypad, [600, 1, 177])
+
+
+@pytest.mark.parametrize("dtype", [H, BF])
+def test_add_long_nonfinite_neighbours(dtype):
+    test_add_nonfinite_neighbours(dtype, [540, 30, 250])
+
+
+def test_add_long_f16_range_and_capture():
+    test_add_f16_range([650, 190])
+    test_capture_and_streams([800, 200])
