@@ -16,12 +16,22 @@
 //                for f16, 128 for bf16), M + zero is subtracted: c - zero, exactly.
 //                The fp32 scale is split into two 16-bit parts, and
 //                w = fl(d * s_hi + fl(d * s_lo)): the product with the fp32 scale
-//                rounded once (f16 bf16: 2^-11, 2^-8), where a scale rounded first
+//                rounded once (f16 2^-11, bf16 2^-8), where a scale rounded first
 //                would add its own error.  The codes of a word are neighbours along
 //                the output axis, so the weights are written as an MN-major operand,
 //                16 bytes per word;
 //   warp 1       kind::f16 MMAs D[128 x N] += W^T dY^T per 128 columns, fp32 in TMEM.
 // The same warps are the epilogue (TMEM lane = column, TMEM column = token).
+// The weights' rounding is the operator's largest error, about that of the rounded result;
+// two MMAs on a weight of two parts would take it away and double the tensor work.
+// f16's range: all weights of a group's column carry one power of two, taken back in the
+// epilogue (it has to be common to everything that is summed).  2^8 suits groups whose
+// largest scale is 6.1e-5 to 1.8; the dequantizing warps note the largest scale on the way,
+// and a CTA that finds another kind goes over its rows again with the power that brings it
+// to [2^7, 2^8) (no lower part of a scale, and with |code - zero| <= 142 no weight, leaves
+// the type).  A pass over the scales first would have cost every call 2 us and more: their
+// rows are a line apiece.  So |w error| <= u |w| + (|code - zero| + 2) 2^-19 of the group's
+// largest scale, u = 2^-11, whatever the sizes of the scales.
 // MT = 2 halves the stages' dY traffic, and where the tiles leave SMs idle the CTAs of a
 // cluster share a tile's rows of W (every split-th stage each) and add up through
 // distributed shared memory in a fixed order; launch_shape picks MT, N and the split.
@@ -121,6 +131,8 @@ constexpr int DT_K = 64;                    // rows of W per stage
 constexpr int DT_GROUP = 4;                 // warps of a dequantizing group
 constexpr int DT_NMAX = 256;
 constexpr int DT_LD = 132;                  // floats of a token's row of staged sums
+// f16: the power of two that weights carry, and the largest scales of a group that it suits
+constexpr float DT_FACTOR = 256.f, DT_TOP_MIN = 0x1p-14f, DT_TOP_MAX = 1.8f;  // 1.8 142 256 < 65504
 
 template <int MT>
 struct DtShape {
@@ -169,6 +181,18 @@ template <> struct DtType<true> {
   __device__ static float back(T2 v) { return __low2float(v); }
 };
 
+// The power of two that brings a group's largest scale to [2^7, 2^8); it and its inverse are
+// normal numbers.
+__device__ __forceinline__ float dt_factor(float top) {
+  const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -119), 126);
+  return __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+}
+
+// 1 / f of a power of two: the exponents add up to 254.
+__device__ __forceinline__ float dt_inverse(float f) {
+  return __uint_as_float((254u << 23) - __float_as_uint(f));
+}
+
 template <bool BF16, int MT, bool SPLIT>
 __global__ void __launch_bounds__(DtShape<MT>::THREADS, 1)
 dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap pmap,
@@ -187,13 +211,18 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
   uint32_t* tmem_slot = (uint32_t*)(done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;
+  // f16, per group of the tile: the largest finite scale (its bits), the factor
+  uint32_t* tops = (uint32_t*)(bars + 16);
+  float* facs = (float*)(tops + 4 * MT);
+  static_assert((3 * S + 1) * 8 + 12 <= 128 && 128 + 8 * 4 * MT <= 256, "fits");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int split = SPLIT ? a.split : 1, part = SPLIT ? (int)blockIdx.x % split : 0;
   const int c0 = (int)blockIdx.x / split * (MT * 128), t0 = blockIdx.y * a.N;
   // stages of this CTA: part, part + split, ..
   const int ns = ((a.n + DT_K - 1) / DT_K - part + split - 1) / split;
-  auto first_row = [&](int it) { return (part + it * split) * DT_K; };
+  auto first_row = [&](int i) { return (part + i * split) * DT_K; };
+  const int g0 = c0 / a.G, ng = (min(c0 + MT * 128, a.k) - 1) / a.G - g0 + 1;  // groups of the tile
   auto stage = [&](int it) { return dt_smem + (size_t)(it % S) * Sh::STAGE; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -204,6 +233,7 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
     tc::mbar_init(done, 1);
     *abort_flag = 0;
     *issued = 0;
+    for (int g = 0; g < 4 * MT; ++g) tops[g] = 0u, facs[g] = BF16 ? 1.f : DT_FACTOR;
     tc::fence_barrier_init();
     tc::prefetch_tensormap(&ymap);
     tc::prefetch_tensormap(&pmap);
@@ -216,135 +246,168 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t bytes = Sh::P + (uint32_t)a.N * DT_K * 2;
-      for (int it = 0; it < ns; ++it) {
-        const int s = it % S;
-        if (it >= S && !tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, a.spin))
-          break;
-        uint8_t* sb = stage(it);
-        tc::mbar_arrive_expect_tx(&full[s], bytes);
-        tc::tma_load_2d(sb + Sh::A + Sh::B, &pmap, &full[s], c0 / 8, first_row(it));
-        tc::tma_load_2d(sb + Sh::A, &ymap, &full[s], first_row(it), t0);
-        *issued = it + 1;
-      }
-    }
-  } else if (warp == 1) {
-    if (tc::elect_one()) {
-      const uint32_t id = tc::instr_desc(BF16 ? 1 : 0, 128, a.N, 1, 0);  // W MN-major, dY K-major
-      const uint32_t s0 = tc::smem_u32(dt_smem);
-      const uint64_t dw = tc::smem_desc_sw128(s0, 8192, 1024);
-      const uint64_t dy = tc::smem_desc_sw128(s0 + Sh::A, 16, 1024);
-      int s = 0;
-      uint32_t ph = 0;
-      for (int it = 0; it < ns; ++it) {
-        // the dequantizing warps waited for the copies before they arrived
-        if (!tc::mbar_wait(&ready[s], ph, abort_flag, a.spin)) break;
-        tc::tc_fence_after();
-        const uint64_t w = tc::desc_add(dw, (uint32_t)s * Sh::STAGE);
-        const uint64_t y = tc::desc_add(dy, (uint32_t)s * Sh::STAGE);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int kk = 0; kk < DT_K / 16; ++kk)
-            tc::mma_f16_ss(tmem + 256 * mt, tc::desc_add(w, mt * 16384 + kk * 2048),
-                           tc::desc_add(y, kk * 32), id, kk > 0 ? 1u : (uint32_t)(it > 0));
-        tc::mma_commit(&empty[s]);
-        if (++s == S) s = 0, ph ^= 1u;
-      }
-      tc::mma_commit(done);  // fires once every MMA issued above has finished
-    }
-  } else {
-    const int grp = (warp - 2) / DT_GROUP, gw = (warp - 2) % DT_GROUP;
-    // quads (32 columns) MT gw .. of rows lane and lane + 32; neighbouring lanes are
-    // neighbouring rows
-    constexpr int R = 2 * MT;
-    // The grids: thread = (row, every second group of the tile) of the group's next stage,
-    // requested a stage of the group ahead and handed round through shared memory.  (Each
-    // thread fetching those of its own runs cost four times the scattered loads: 32 rows
-    // are 32 lines, and the L1 looks up one a cycle.)
-    const int gt = gw * 32 + lane, grow = gt % DT_K, ghalf = gt / DT_K;
-    const int g0 = c0 / a.G, ng = (min(c0 + MT * 128, a.k) - 1) / a.G - g0 + 1;
-    float* gsc = (float*)(grids + grp * Sh::GRID);                              // [4 MT][64]
-    typename Ty::T* gze = (typename Ty::T*)(grids + grp * Sh::GRID + MT * 4 * DT_K * 4);
-    float fs[R];
-    int fz[R];
-    auto fetch = [&](int it) {
-      const int j = first_row(it) + grow;
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const bool ok = ghalf + 2 * i < ng && it < ns && j < a.n;
-        const int64_t at = (int64_t)j * a.ngroups + g0 + ghalf + 2 * i;
-        fs[i] = ok ? __ldg(a.scales + at) : 0.f;
-        fz[i] = ok ? __ldg(a.zeros + at) : 0;
-      }
-    };
-    int gq[MT];  // the group slot of each quad
-#pragma unroll
-    for (int q = 0; q < MT; ++q) gq[q] = min(c0 + 32 * (MT * gw + q), a.k - 1) / a.G - g0;
-    fetch(grp);
-    bool gave_up = false;
-    for (int it = grp; it < ns; it += S) {
-      const int s = it % S;
-      // the last stage's grids are read; a give-up ends the loop of the whole group
-      if (tc::named_bar_any(1 + grp, 32 * DT_GROUP, gave_up)) break;
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (ghalf + 2 * i < ng) {
-          gsc[(ghalf + 2 * i) * DT_K + grow] = fs[i];
-          gze[(ghalf + 2 * i) * DT_K + grow] = Ty::one(Ty::BASE + (float)fz[i]);  // exact, |zero| <= 127
+  // stages of earlier passes: a second one follows where the factors did not suit (f16)
+  int base = 0;
+  for (;;) {
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint32_t bytes = Sh::P + (uint32_t)a.N * DT_K * 2;
+        for (int i = 0; i < ns; ++i) {
+          const int it = base + i, s = it % S;
+          if (it >= S && !tc::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, abort_flag, a.spin))
+            break;
+          uint8_t* sb = stage(it);
+          tc::mbar_arrive_expect_tx(&full[s], bytes);
+          tc::tma_load_2d(sb + Sh::A + Sh::B, &pmap, &full[s], c0 / 8, first_row(i));
+          tc::tma_load_2d(sb + Sh::A, &ymap, &full[s], first_row(i), t0);
+          *issued = it + 1;
         }
-      tc::named_bar_sync(1 + grp, 32 * DT_GROUP);
-      fetch(it + S);
-      T2 hi[R], lo[R], zz[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int at = gq[r / 2] * DT_K + lane + 32 * (r & 1);
-        const float sc = gsc[at];
-        hi[r] = Ty::pair(sc);
-        lo[r] = Ty::pair(sc - Ty::back(hi[r]));
-        zz[r] = Ty::both(gze[at]);
       }
-      if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin)) {
-        gave_up = true;
-        continue;
+    } else if (warp == 1) {
+      if (tc::elect_one()) {
+        const uint32_t id = tc::instr_desc(BF16 ? 1 : 0, 128, a.N, 1, 0);  // W MN-major, dY K-major
+        const uint32_t s0 = tc::smem_u32(dt_smem);
+        const uint64_t dw = tc::smem_desc_sw128(s0, 8192, 1024);
+        const uint64_t dy = tc::smem_desc_sw128(s0 + Sh::A, 16, 1024);
+        int s = base % S;
+        uint32_t ph = (uint32_t)(base / S) & 1u;
+        for (int i = 0; i < ns; ++i) {
+          // the dequantizing warps waited for the copies before they arrived
+          if (!tc::mbar_wait(&ready[s], ph, abort_flag, a.spin)) break;
+          tc::tc_fence_after();
+          const uint64_t w = tc::desc_add(dw, (uint32_t)s * Sh::STAGE);
+          const uint64_t y = tc::desc_add(dy, (uint32_t)s * Sh::STAGE);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int kk = 0; kk < DT_K / 16; ++kk)
+              tc::mma_f16_ss(tmem + 256 * mt, tc::desc_add(w, mt * 16384 + kk * 2048),
+                             tc::desc_add(y, kk * 32), id, kk > 0 ? 1u : (uint32_t)(i > 0));
+          tc::mma_commit(&empty[s]);
+          if (++s == S) s = 0, ph ^= 1u;
+        }
       }
-      uint8_t* sb = stage(it);
+    } else {
+      const int grp = (warp - 2) / DT_GROUP, gw = (warp - 2) % DT_GROUP;
+      // quads (32 columns) MT gw .. of rows lane and lane + 32; neighbouring lanes are
+      // neighbouring rows
+      constexpr int R = 2 * MT;
+      // The grids: thread = (row, every second group of the tile) of the group's next stage,
+      // requested a stage of the group ahead and handed round through shared memory.  (Each
+      // thread fetching those of its own runs cost four times the scattered loads: 32 rows
+      // are 32 lines, and the L1 looks up one a cycle.)
+      const int gt = gw * 32 + lane, grow = gt % DT_K, ghalf = gt / DT_K;
+      float* gsc = (float*)(grids + grp * Sh::GRID);                              // [4 MT][64]
+      typename Ty::T* gze = (typename Ty::T*)(grids + grp * Sh::GRID + MT * 4 * DT_K * 4);
+      float fs[R];
+      int fz[R];
+      float fac[R];
+      uint32_t top[R];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int j = lane + 32 * (r & 1), quad = MT * gw + r / 2;
-        const int pos = MT == 2 ? j * 128 + ((quad ^ (j & 7)) << 4)          // 128-byte swizzle
-                                : j * 64 + ((quad ^ ((j >> 1) & 3)) << 4);   // 64-byte swizzle
-        const uint4 pw = *reinterpret_cast<const uint4*>(sb + Sh::A + Sh::B + pos);
-        const uint32_t words[4] = {pw.x, pw.y, pw.z, pw.w};
-        uint8_t* row = sb + (quad / 2) * 8192 + j * 128;  // 64-column atoms
+      for (int i = 0; i < R; ++i) fac[i] = facs[ghalf + 2 * i], top[i] = 0u;
+      auto fetch = [&](int st) {
+        const int j = first_row(st) + grow;
 #pragma unroll
-        for (int wi = 0; wi < 4; ++wi) {
-          const uint32_t w = words[wi], w4 = w >> 4;
-          uint32_t o[4];
+        for (int i = 0; i < R; ++i) {
+          const bool ok = ghalf + 2 * i < ng && st < ns && j < a.n;
+          const int64_t at = (int64_t)j * a.ngroups + g0 + ghalf + 2 * i;
+          fs[i] = ok ? __ldg(a.scales + at) : 0.f;
+          fz[i] = ok ? __ldg(a.zeros + at) : 0;
+        }
+      };
+      int gq[MT];  // the group slot of each quad
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // byte i of w (c_2i low) into half 0, byte i of w >> 4 (c_2i+1 low) into half 1
-            const uint32_t v =
-                __byte_perm(w, w4, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | (i << 12)));
-            const uint32_t h = (v & 0x000F000Fu) | Ty::MAGIC;               // M + c, exact
-            const T2 d = __hsub2(*reinterpret_cast<const T2*>(&h), zz[r]);  // c - zero, exact
-            const T2 x = __hfma2(d, hi[r], __hmul2(d, lo[r]));
-            o[i] = *reinterpret_cast<const uint32_t*>(&x);
+      for (int q = 0; q < MT; ++q) gq[q] = min(c0 + 32 * (MT * gw + q), a.k - 1) / a.G - g0;
+      int st = (grp - base % S + S) % S;  // the group's stages of this pass
+      fetch(st);
+      bool gave_up = false;
+      for (; st < ns; st += S) {
+        const int it = base + st, s = it % S;
+        // the last stage's grids are read; a give-up ends the loop of the whole group
+        if (tc::named_bar_any(1 + grp, 32 * DT_GROUP, gave_up)) break;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (ghalf + 2 * i < ng) {
+            if (!BF16) {
+              const uint32_t t = __float_as_uint(fs[i]) & 0x7fffffffu;
+              if (t < 0x7f800000u) top[i] = max(top[i], t);
+            }
+            gsc[(ghalf + 2 * i) * DT_K + grow] = BF16 ? fs[i] : fs[i] * fac[i];
+            gze[(ghalf + 2 * i) * DT_K + grow] = Ty::one(Ty::BASE + (float)fz[i]);  // exact, |zero| <= 127
           }
-          *reinterpret_cast<uint4*>(row + ((((quad % 2) * 4 + wi) ^ (j & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+        tc::named_bar_sync(1 + grp, 32 * DT_GROUP);
+        fetch(st + S);
+        T2 hi[R], lo[R], zz[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int at = gq[r / 2] * DT_K + lane + 32 * (r & 1);
+          const float sc = gsc[at];
+          hi[r] = Ty::pair(sc);
+          const float h = Ty::back(hi[r]);
+          lo[r] = Ty::pair(isfinite(h) ? sc - h : 0.f);  // an infinity stays one
+          zz[r] = Ty::both(gze[at]);
+        }
+        if (!tc::mbar_wait_warp(&full[s], (uint32_t)(it / S) & 1u, abort_flag, a.spin)) {
+          gave_up = true;
+          continue;
+        }
+        uint8_t* sb = stage(it);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int j = lane + 32 * (r & 1), quad = MT * gw + r / 2;
+          const int pos = MT == 2 ? j * 128 + ((quad ^ (j & 7)) << 4)          // 128-byte swizzle
+                                  : j * 64 + ((quad ^ ((j >> 1) & 3)) << 4);   // 64-byte swizzle
+          const uint4 pw = *reinterpret_cast<const uint4*>(sb + Sh::A + Sh::B + pos);
+          const uint32_t words[4] = {pw.x, pw.y, pw.z, pw.w};
+          uint8_t* row = sb + (quad / 2) * 8192 + j * 128;  // 64-column atoms
+#pragma unroll
+          for (int wi = 0; wi < 4; ++wi) {
+            const uint32_t w = words[wi], w4 = w >> 4;
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // byte i of w (c_2i low) into half 0, byte i of w >> 4 (c_2i+1 low) into half 1
+              const uint32_t v =
+                  __byte_perm(w, w4, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | (i << 12)));
+              const uint32_t h = (v & 0x000F000Fu) | Ty::MAGIC;               // M + c, exact
+              const T2 d = __hsub2(*reinterpret_cast<const T2*>(&h), zz[r]);  // c - zero, exact
+              const T2 x = __hfma2(d, hi[r], __hmul2(d, lo[r]));
+              o[i] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(row + ((((quad % 2) * 4 + wi) ^ (j & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        tc::fence_proxy_async_smem();  // the MMA reads what this thread wrote
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ready[s]);
+      }
+      if (!BF16) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {  // ghalf is the warp's
+          const uint32_t t = __reduce_max_sync(0xffffffffu, top[i]);
+          if (lane == 0 && t != 0u) atomicMax(&tops[ghalf + 2 * i], t);
         }
       }
-      tc::fence_proxy_async_smem();  // the MMA reads what this thread wrote
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&ready[s]);
     }
+    __syncthreads();
+    if (BF16 || base > 0 || *abort_flag) break;
+    bool again = false;
+    for (int g = 0; g < ng; ++g) {
+      const float t = __uint_as_float(tops[g]);
+      again |= t > 0.f && !(t >= DT_TOP_MIN && t <= DT_TOP_MAX);
+    }
+    if (!again) break;
+    if (threadIdx.x < ng && tops[threadIdx.x] != 0u)
+      facs[threadIdx.x] = dt_factor(__uint_as_float(tops[threadIdx.x]));
+    __syncthreads();
+    base = ns;
   }
-  // (the barrier first: the idle lanes of the copying and the issuing warp, polling beside
-  // their one busy lane, slowed the kernel by a seventh)
-  __syncthreads();
+  if (warp == 1) {
+    if (tc::elect_one()) tc::mma_commit(done);  // the lane that issued them: fires when all are over
+  }
+  // (the barrier comes before this wait: the idle lanes of the copying and the issuing warp,
+  // polling beside their one busy lane, slowed the kernel by a seventh)
   // all MMAs done (shared memory is free for the sums), all copies landed
   const bool finished = tc::mbar_wait_warp(done, 0, abort_flag, tc::kSpinLimit);
   if (*abort_flag && threadIdx.x == 0)
@@ -362,6 +425,8 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
       const int mt = x / nch, q = x % nch * 32;
       const int c = c0 + mt * 128 + quarter * 32 + lane;
       typename Ty::T* out = reinterpret_cast<typename Ty::T*>(a.dX) + c;
+      // one over the power of two that this column's weights carry
+      const float inv = BF16 ? 1.f : dt_inverse(facs[min(c - lane, a.k - 1) / a.G - g0]);
       float v[32];
       tc::tmem_ld_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(256 * mt + q), v);
       tc::tmem_ld_wait();
@@ -370,12 +435,13 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
         for (int t = 0; t < 32; ++t)
           if (c < a.k && q + t < a.N && t0 + q + t < a.m)
             out[(int64_t)(t0 + q + t) * a.lddx] =
-                dg_out<typename Ty::T>(ok ? v[t] : __int_as_float(0x7fc00000));
+                dg_out<typename Ty::T>(ok ? v[t] * inv : __int_as_float(0x7fc00000));
       } else {
 #pragma unroll
         for (int t = 0; t < 32; ++t)
           if (q + t < a.N)
-            sums[(q + t) * DT_LD + quarter * 32 + lane] = ok ? v[t] : __int_as_float(0x7fc00000);
+            sums[(q + t) * DT_LD + quarter * 32 + lane] =
+                ok ? v[t] * inv : __int_as_float(0x7fc00000);
       }
     }
   }
