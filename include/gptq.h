@@ -359,7 +359,8 @@ GPTQ_API gptq_status gptq_rotate(const void* in, gptq_dtype dt, int64_t rows, in
  *   4-bit, g_idx NULL, group_size a multiple of 32 (or one group per row), dY
  *     16-byte aligned with lddy % 8 == 0 and qweight 16-byte aligned: the
  *     tensor-core kernel (each weight formed from the fp32 scale and rounded
- *     once to dt; |zeros| <= 127; fp32 accumulation).  f16: the weights of a
+ *     once to dt; fp32 accumulation).  It holds zeros of -127 .. 127; another
+ *     one makes the columns of its group NaN.  f16: the weights of a
  *     group carry a power of two that suits its scales, so scales of any size
  *     keep that rounding, to (|code - zero| + 2) 2^-19 of the largest scale of
  *     the group over the n rows; a group whose largest is outside [2^-14, 1.8]

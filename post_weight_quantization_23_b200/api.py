@@ -208,7 +208,8 @@ def quant_matmul_dgrad(dY: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The gradient of quant_matmul with respect to its input, dX = dY W_hat, read
     straight from the packed weights (gptq_gemm_dgrad): dY (m, n) f16/bf16 on the
-    device, the weights as for quant_matmul.  Returns dX (m, k) in dY's dtype
+    device, the weights as for quant_matmul (4-bit weights without g_idx: zeros of
+    -127 .. 127, a group with another one gives NaN).  Returns dX (m, k) in dY's dtype
     (``out`` if given)."""
     return _lib.on_stream("gptq_gemm_dgrad", stream, dY, (_lib._ops or _lib.ops()).gemm_dgrad, dY,
                           qweight, scales, zeros, bits, group_size, k, g_idx, out)

@@ -131,6 +131,9 @@ constexpr int DT_K = 64;                    // rows of W per stage
 constexpr int DT_GROUP = 4;                 // warps of a dequantizing group
 constexpr int DT_NMAX = 256;
 constexpr int DT_LD = 132;                  // floats of a token's row of staged sums
+// zeros up to this magnitude are exact in 128 + zero and code - zero of bf16; a group that holds
+// another one becomes NaN
+constexpr int DT_ZERO = 127;
 // f16: the power of two that weights carry, and the largest scales of a group that it suits
 constexpr float DT_FACTOR = 256.f, DT_TOP_MIN = 0x1p-14f, DT_TOP_MAX = 1.8f;  // 1.8 142 256 < 65504
 
@@ -332,8 +335,10 @@ dgrad_tc_kernel(const __grid_constant__ CUtensorMap ymap, const __grid_constant_
               const uint32_t t = __float_as_uint(fs[i]) & 0x7fffffffu;
               if (t < 0x7f800000u) top[i] = max(top[i], t);
             }
-            gsc[(ghalf + 2 * i) * DT_K + grow] = BF16 ? fs[i] : fs[i] * fac[i];
-            gze[(ghalf + 2 * i) * DT_K + grow] = Ty::one(Ty::BASE + (float)fz[i]);  // exact, |zero| <= 127
+            const bool fits = fz[i] >= -DT_ZERO && fz[i] <= DT_ZERO;
+            gsc[(ghalf + 2 * i) * DT_K + grow] =
+                !fits ? __int_as_float(0x7fc00000) : BF16 ? fs[i] : fs[i] * fac[i];
+            gze[(ghalf + 2 * i) * DT_K + grow] = Ty::one(Ty::BASE + (float)fz[i]);  // exact where it fits
           }
         tc::named_bar_sync(1 + grp, 32 * DT_GROUP);
         fetch(st + S);

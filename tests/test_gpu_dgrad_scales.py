@@ -152,6 +152,34 @@ def test_scales_of_mixed_sizes(case, dtype):
 
 @pytest.mark.parametrize("dtype", [H, BF])
 @pytest.mark.parametrize("case", [ONE, SPLIT, TWO, GENERAL], ids=["one", "split", "two", "general"])
+@pytest.mark.parametrize("scale", [0.01, 1e-6])
+def test_zeros_out_of_range(case, scale, dtype):
+    # the tensor-core kernel holds zeros up to +-127 exactly; a group that has another is NaN.
+    # The general kernel takes any.
+    n, k, G, m = case
+    scales = _scales(n, k, G, 5, 0.6 * scale, 1.4 * scale)
+    dY, qw, codes, zeros = _inputs(n, k, G, m, dtype, scales, 6, min(0.01 / scale, 1e3))
+    ng = zeros.shape[1]
+    zeros[n - 1, 0] = 127
+    zeros[3, 0] = -127
+    zeros[5, 1] = 300
+    zeros[n // 2, ng - 1] = -128
+    zeros[7, ng - 2] = 1 << 30
+    got = _run(dY, qw, scales, zeros, G, k)
+    ref, bound = _ref(dY, codes, scales, zeros, G, dtype, case is not GENERAL)
+    if case is GENERAL:
+        ok = ref.abs() < 6e4
+        _check(got[ok], ref[ok], bound[ok])
+        return
+    bad = torch.zeros(k, dtype=torch.bool, device="cuda")
+    for g in (1, ng - 2, ng - 1):
+        bad[g * G:(g + 1) * G] = True
+    assert got[:, bad].isnan().all()
+    _check(got[:, ~bad], ref[:, ~bad], bound[:, ~bad])
+
+
+@pytest.mark.parametrize("dtype", [H, BF])
+@pytest.mark.parametrize("case", [ONE, SPLIT, TWO, GENERAL], ids=["one", "split", "two", "general"])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 def test_nonfinite_scales_stay_in_their_group(case, bad, dtype):
     n, k, G, m = case
