@@ -420,7 +420,9 @@ GPTQ_API gptq_status gptq_lora_add(const void* Y, int64_t ldy, const void* X, gp
  *   out      (m, k) dt, or NULL: no input gradient (the lowest layer); rows
  *            outside the requests are left as they are.
  *   dA       (na, rank, k), dB (na, n, rank) dt out, contiguous, written whole
- *            (0 for an adapter without rows).
+ *            (0 for an adapter without rows).  A NaN or an infinity in a row of
+ *            dY, X or V makes the sums that it enters NaN or infinite (an
+ *            infinity may give NaN: the factors enter in two parts), no others.
  *   ws       GPTQ_OP_LORA_BACKWARD workspace.
  * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_UNSUPPORTED (rank, f32),
  * GPTQ_ERR_WORKSPACE, GPTQ_ERR_CUDA. */

@@ -348,9 +348,10 @@ lora_decode_kernel(LoraArgs a, int yvec, int late) {
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < LORA_CLUSTER; ++c) s += part[c * PS + e];
-        s *= sc;
-        vs[e] = s;
+        // columns that only pad the rank stay 0 where an infinity met their zeros
         const int tk = e / RP, p = e % RP;
+        s = p < a.r ? s * sc : 0.f;
+        vs[e] = s;
         if (a.V != nullptr && rank == 0 && sm.row[tk] >= 0 && p < a.r)
           a.V[(int64_t)sm.row[tk] * a.r + p] = s;
       }

@@ -364,12 +364,14 @@ lora_tc_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
               const float4 w = part[c * OWN4 + e];
               v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
             }
+            const int r = e / (RP / 4);
+            const int c4 = RP == 16 ? (e % (RP / 4)) ^ ((r >> 1) & 3) : (e % (RP / 4)) ^ (r & 7);
             v.x *= sc, v.y *= sc, v.z *= sc, v.w *= sc;
+            // columns that only pad the rank stay 0 where an infinity met their zeros
+            if (4 * c4 >= a.r) v = make_float4(0.f, 0.f, 0.f, 0.f);
             const uint32_t va = tc::smem_u32(vbuf) + 16u * (uint32_t)(rank * OWN4 + e);
 #pragma unroll
             for (int c = 0; c < CS; ++c) cluster_st_f4(cluster_map(va, (uint32_t)c), v);
-            const int r = e / (RP / 4);
-            const int c4 = RP == 16 ? (e % (RP / 4)) ^ ((r >> 1) & 3) : (e % (RP / 4)) ^ (r & 7);
             if (a.V != nullptr && rank * OWNED + r < pc.cnt && 4 * c4 < a.r) {  // r % 8 == 0
               float* o = a.V + (int64_t)(pc.t0 + rank * OWNED + r) * a.r + 4 * c4;
               o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
