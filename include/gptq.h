@@ -353,7 +353,7 @@ GPTQ_API gptq_status gptq_rotate(const void* in, gptq_dtype dt, int64_t rows, in
  *   dY      (m, n) f16 or bf16 (dt), row-major, leading dimension lddy >= n.
  *   qweight, scales, zeros, g_idx, bits, group_size, ngroups  as for gptq_gemm.
  *   dX      (m, k) out, dt, row-major, leading dimension lddx >= k.  Must not
- *           overlap dY.
+ *           overlap dY (ranges of columns of one buffer do not).
  *   m <= 131070 tokens.  The library allocates nothing.
  * Kernel choice:
  *   4-bit, g_idx NULL, group_size a multiple of 32 (or one group per row), dY
@@ -387,7 +387,8 @@ GPTQ_API gptq_status gptq_gemm_dgrad(const void* dY, gptq_dtype dt, int64_t m, i
  *             [0, m]; overlapping requests give unspecified rows, never an
  *             access outside the batch.
  *   Y        (m, n) dt or NULL (then out = B_a V); ldy >= n.  May be out itself
- *            (with ldy == ldo); other overlaps of out with Y or X are rejected.
+ *            (with ldy == ldo); other overlaps of out with Y or X are rejected
+ *            (ranges of columns of one buffer, all with its row pitch, are apart).
  *            Rows of a request without an adapter get a copy of Y (0 if NULL).
  *   X        (m, k) f16 or bf16 (dt), ldx >= k.
  *   A        (na, rank, k) dt, B (na, n, rank) dt, contiguous; scaling fp32[na].
@@ -416,7 +417,7 @@ GPTQ_API gptq_status gptq_lora_add(const void* Y, int64_t ldy, const void* X, gp
  *   V        (m, rank) fp32 from gptq_lora_add.
  *   A, B, scaling, na, rank, starts, adapter, nreq  as in the forward pass.
  *   dX       (m, k) dt or NULL (then out = A_a^T U), may be out itself; other
- *            overlaps of out with dX or dY are rejected.
+ *            overlaps of out with dX, dY or X are rejected.
  *   out      (m, k) dt, or NULL: no input gradient (the lowest layer); rows
  *            outside the requests are left as they are.
  *   dA       (na, rank, k), dB (na, n, rank) dt out, contiguous, written whole

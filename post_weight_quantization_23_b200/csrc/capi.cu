@@ -84,13 +84,21 @@ size_t dtype_bytes(gptq_dtype dt) { return dt == GPTQ_F32 ? 4 : 2; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 27;  // rows of an adapter or checkpoint call
 
-// Whether two (rows, cols) matrices of `ea`, `eb` bytes per element share memory.
+// Whether two (rows, cols) matrices of `ea`, `eb` bytes per element share memory.  Rows with
+// the same pitch in bytes are compared within the pitch: two ranges of columns of one buffer
+// are apart.  With different pitches, whole extents are compared.
 bool overlap(const void* a, int64_t lda, int64_t ca, size_t ea, const void* b, int64_t ldb,
              int64_t cb, size_t eb, int64_t rows) {
   if (a == nullptr || b == nullptr || rows <= 0 || ca <= 0 || cb <= 0) return false;
   const char *pa = (const char*)a, *pb = (const char*)b;
-  const size_t na = ((size_t)(rows - 1) * lda + ca) * ea, nb = ((size_t)(rows - 1) * ldb + cb) * eb;
-  return pa < pb + nb && pb < pa + na;
+  const size_t wa = ca * ea, wb = cb * eb, pitch = lda * ea;
+  const size_t na = (size_t)(rows - 1) * lda * ea + wa, nb = (size_t)(rows - 1) * ldb * eb + wb;
+  if (pa >= pb + nb || pb >= pa + na) return false;
+  if (pitch != ldb * eb) return true;
+  // b's rows begin `d` bytes behind the beginning of one of a's (counted on without end)
+  const size_t d = pb >= pa ? (size_t)(pb - pa) % pitch
+                            : (pitch - (size_t)(pa - pb) % pitch) % pitch;
+  return d < wa || d + wb > pitch;
 }
 
 // The checks that the forward and the backward call of the adapters share.
