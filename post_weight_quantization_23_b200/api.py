@@ -228,7 +228,12 @@ def lora_add(Y, X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: torc
     Without ``out`` Y (m, n) is updated in place; Y may be None when ``out`` is
     given.  ``V`` (m, rank) fp32, if given, receives scaling_a A_a x_t, which
     lora_backward needs.  Rows outside the requests are left as they are.
-    Returns the updated tensor."""
+    Returns the updated tensor.
+
+    Nothing is recorded for autograd (as for every call of this module): the
+    gradients are lora_backward's and quant_matmul_dgrad's.  A tensor that is
+    written here has its version raised, and is refused if it requires grad while
+    grad mode is on."""
     return _lib.on_stream("gptq_lora_add", stream, X, (_lib._ops or _lib.ops()).lora_add, Y, X, A, B,
                           scaling, starts, adapter, out, V)
 

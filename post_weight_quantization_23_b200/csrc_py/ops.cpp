@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -103,6 +104,29 @@ gptq_dtype dtype_code(const at::Tensor& t) {
   }
 }
 
+// A tensor of the caller's that the call writes.  The calls record nothing for autograd, so
+// under grad mode an update of a tensor that requires grad would be missing from its gradients:
+// refused, as torch refuses it for out= arguments.
+const at::Tensor& target(const char* name, const at::Tensor& t) {
+  if (c10::GradMode::is_enabled() && t.requires_grad())
+    refuse(std::string(name) + ": written, and requires grad (call it under torch.no_grad() or "
+           "inside an autograd.Function)");
+  return t;
+}
+const at::Tensor* target(const char* name, const at::Tensor* t) {
+  if (t != nullptr) target(name, *t);
+  return t;
+}
+
+// Such a tensor has changed: an autograd graph that saved it finds out.  (An inference tensor
+// has no version.)
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void changed(const at::Tensor* t) {
+  if (t != nullptr) changed(*t);
+}
+
 at::Tensor make(at::IntArrayRef sizes, const at::Tensor& like, at::ScalarType dt) {
   return at::empty(sizes, like.options().dtype(dt).requires_grad(false));
 }
@@ -174,9 +198,10 @@ PyObject* given(PyObject* o) {
 GPTQ_ENTRY(lora_add, "gptq_lora_add") {
   count(n, 9);
   Device dev;
-  const at::Tensor &X = tensor(a[1], "X"), *Y = optional(a[0], "Y"), *V = optional(a[8], "V");
-  PyObject* target = a[7] != Py_None ? a[7] : a[0];
-  const at::Tensor& out = tensor(target, "Y or out");
+  const at::Tensor &X = tensor(a[1], "X"), *Y = optional(a[0], "Y"),
+                   *V = target("V", optional(a[8], "V"));
+  PyObject* to = a[7] != Py_None ? a[7] : a[0];
+  const at::Tensor& out = target("Y or out", tensor(to, "Y or out"));
   const at::ScalarType dt = X.scalar_type();
   const gptq_dtype code = dtype_code(X);
   const Adapters d = adapters(a + 2, dt, dev);
@@ -190,7 +215,9 @@ GPTQ_ENTRY(lora_add, "gptq_lora_add") {
                          d.A, d.B, d.scaling, d.na, (int)d.r, d.starts, d.adapter, d.nreq, d.n,
                          out.data_ptr(), ldo, pv, s);
   });
-  return given(target);
+  changed(out);
+  changed(V);
+  return given(to);
 }
 
 // dY, X, V, A, B, scaling, starts, adapter, dX, x_scales, out, dA, dB, ws -> (out, dA, dB)
@@ -199,8 +226,8 @@ GPTQ_ENTRY(lora_backward, "gptq_lora_backward") {
   Device dev;
   const at::Tensor &dY = tensor(a[0], "dY"), &X = tensor(a[1], "X"), &V = tensor(a[2], "V");
   const at::Tensor *dX = optional(a[8], "dX"), *xs = optional(a[9], "x_scales");
-  PyObject* target = a[10] != Py_None ? a[10] : a[8];
-  const at::Tensor* out = optional(target, "out");
+  PyObject* to = a[10] != Py_None ? a[10] : a[8];
+  const at::Tensor* out = target("dX or out", optional(to, "out"));
   const at::ScalarType dt = dY.scalar_type();
   const gptq_dtype code = dtype_code(dY);
   const Adapters d = adapters(a + 3, dt, dev);
@@ -213,8 +240,8 @@ GPTQ_ENTRY(lora_backward, "gptq_lora_backward") {
   const float* pv = whole<float>("V", V, {m, d.r}, at::kFloat, dev);
   const int64_t ldo = out != nullptr ? matrix("out", *out, m, d.k, dt, dev) : 0;
   const int64_t ldd = out != nullptr && dX != nullptr ? matrix("dX", *dX, m, d.k, dt, dev) : 0;
-  const at::Tensor *gA = optional(a[11], "dA"), *gB = optional(a[12], "dB"),
-                   *ws = optional(a[13], "ws");
+  const at::Tensor *gA = target("dA", optional(a[11], "dA")),
+                   *gB = target("dB", optional(a[12], "dB")), *ws = target("ws", optional(a[13], "ws"));
   const at::Tensor dA = gA != nullptr ? *gA : make({d.na, d.r, d.k}, dY, dt);
   const at::Tensor dB = gB != nullptr ? *gB : make({d.na, d.n, d.r}, dY, dt);
   void* pa = whole<void>("dA", dA, {d.na, d.r, d.k}, dt, dev);
@@ -230,9 +257,13 @@ GPTQ_ENTRY(lora_backward, "gptq_lora_backward") {
         out != nullptr && dX != nullptr ? dX->data_ptr() : nullptr, ldd,
         out != nullptr ? out->data_ptr() : nullptr, ldo, pa, pb, w.data_ptr(), w.nbytes(), s);
   });
+  changed(out);
+  changed(gA);
+  changed(gB);
+  changed(ws);
   PyObject* res = PyTuple_New(3);
   if (res == nullptr) return nullptr;
-  PyTuple_SET_ITEM(res, 0, given(target));
+  PyTuple_SET_ITEM(res, 0, given(to));
   PyTuple_SET_ITEM(res, 1, gA != nullptr ? given(a[11]) : THPVariable_Wrap(dA));
   PyTuple_SET_ITEM(res, 2, gB != nullptr ? given(a[12]) : THPVariable_Wrap(dB));
   return res;
@@ -243,7 +274,8 @@ GPTQ_ENTRY(act_checkpoint, "gptq_act_checkpoint") {
   count(n, 3);
   Device dev;
   const at::Tensor& X = tensor(a[0], "X");
-  const at::Tensor *gc = optional(a[1], "codes"), *gs = optional(a[2], "scales");
+  const at::Tensor *gc = target("codes", optional(a[1], "codes")),
+                   *gs = target("scales", optional(a[2], "scales"));
   const gptq_dtype code = dtype_code(X);
   if (X.dim() != 2) refuse("X: (m, k)");
   const int64_t m = X.size(0), k = X.size(1), nb = (k + 127) / 128;
@@ -256,6 +288,8 @@ GPTQ_ENTRY(act_checkpoint, "gptq_act_checkpoint") {
     return gptq_act_checkpoint(X.data_ptr(), code, m, k, ldx,
                                static_cast<int8_t*>(codes.data_ptr()), ldc, ps, s);
   });
+  changed(gc);
+  changed(gs);
   PyObject* res = PyTuple_New(2);
   if (res == nullptr) return nullptr;
   PyTuple_SET_ITEM(res, 0, gc != nullptr ? given(a[1]) : THPVariable_Wrap(codes));
@@ -268,7 +302,7 @@ GPTQ_ENTRY(act_restore, "gptq_act_restore") {
   count(n, 4);
   Device dev;
   const at::Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
-  const at::Tensor* go = optional(a[3], "out");
+  const at::Tensor* go = target("out", optional(a[3], "out"));
   if (codes.dim() != 2) refuse("codes: (m, k)");
   if (go == nullptr && !THPDtype_Check(a[2])) refuse("dtype: not a torch.dtype");
   const int64_t m = codes.size(0), k = codes.size(1);
@@ -282,6 +316,7 @@ GPTQ_ENTRY(act_restore, "gptq_act_restore") {
     return gptq_act_restore(static_cast<const int8_t*>(codes.data_ptr()), ldc, ps, m, k, code,
                             out.data_ptr(), ldo, s);
   });
+  changed(go);
   return go != nullptr ? given(a[3]) : THPVariable_Wrap(out);
 }
 
@@ -293,7 +328,7 @@ GPTQ_ENTRY(gemm_dgrad, "gptq_gemm_dgrad") {
                    &sc = tensor(a[2], "scales"), &ze = tensor(a[3], "zeros");
   const int64_t bits = integer(a[4], "bits"), group = integer(a[5], "group_size"),
                 k = integer(a[6], "k");
-  const at::Tensor *gi = optional(a[7], "g_idx"), *go = optional(a[8], "out");
+  const at::Tensor *gi = optional(a[7], "g_idx"), *go = target("out", optional(a[8], "out"));
   const gptq_dtype code = dtype_code(dY);
   if (dY.dim() != 2 || sc.dim() != 2) refuse("dY (m, n), scales (n, ngroups)");
   if (bits != 2 && bits != 3 && bits != 4 && bits != 8)
@@ -311,6 +346,7 @@ GPTQ_ENTRY(gemm_dgrad, "gptq_gemm_dgrad") {
     return gptq_gemm_dgrad(dY.data_ptr(), code, m, nn, ldy, pq, ps, pz, pg, k, (int)bits, (int)group,
                            ng, out.data_ptr(), ldx, s);
   });
+  changed(go);
   return go != nullptr ? given(a[8]) : THPVariable_Wrap(out);
 }
 
