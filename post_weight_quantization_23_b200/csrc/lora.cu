@@ -480,12 +480,23 @@ gptq_status lora_general(const LoraArgs& a, bool bf16, bool backward, cudaStream
 // Batches of up to this many rows go to the decode kernel whole; in larger ones it
 // takes the requests of up to LORA_SHORT rows.  (A tensor-core piece costs its 128 rows
 // whatever it holds, 10 us and more through the exchange; three pieces of 8 rows less.)
-// The decode kernel's time grows with every 8 rows and with the rank, the other's hardly.
-// One request, decode against tensor cores: rank 16, 4096 -> 4096, 256 rows 7.6 and 15.1 us,
-// 768 rows 14.4 and 15.1; rank 32, 11008 -> 4096, 512 rows 17.8 and 18.5, 640 rows 22.7 and
-// 19.1; rank 64, 4096 -> 11008, 257 rows 17.1 and 25.4, 384 rows 27.4 and 25.3; rank 128,
-// 4096 -> 4096, 192 rows 19.9 and 23.7, 256 rows 27.4 and 23.8.
-constexpr int lora_decode_rows(int r) { return r <= 16 ? 704 : r <= 32 ? 512 : r <= 64 ? 256 : 192; }
+// The tensor-core kernel's time hardly depends on the rows; the decode kernel's grows with the
+// rank and by a step wherever its pieces need another CTA per SM (33 pieces of 8 rows each), and
+// that step, not the layer's width or the number of adapters, is where the two meet.  Decode
+// against tensor cores in us, 4096 -> 4096 and 4096 -> 11008, one request:
+//   rank 16   512 rows 11.0 : 12.8 and 16.7 : 20.5,   536 rows 13.7 : 12.9 and 22.5 : 20.7
+//   rank 32   512 rows 13.9 : 13.9 and 20.4 : 21.8,   544 rows 17.3 : 14.0 and 26.7 : 22.0
+//   rank 64   256 rows 11.1 : 15.0 and 15.8 : 22.6,   288 rows 16.5 : 15.0 and 24.9 : 22.7
+//   rank 128  192 rows 18.1 : 20.9 and 26.6 : 31.5,   256 rows 25.4 : 20.9 and 39.8 : 31.7
+// Four requests on four adapters: within 0.5 of these, but for 4096 -> 11008 at rank 64, 256 rows
+// 19.5 : 22.6, and at rank 128, 192 rows 36.1 : 33.6.  2048 -> 2048: within 1 us of each other
+// at the rule's edges but for rank 128 (192 rows 14.5 : 17.0).
+// Several requests may all be short, and then both kernels run, the one for nothing: at rank 16
+// and 4096 -> 4096 the decode kernel alone against the two takes 16.1 : 20.7 us for 40 requests
+// of 15 rows, 29.4 : 44.2 for 600 of one, 15.8 : 13.4 for 6 of 100 (the host does not know).
+constexpr int lora_decode_rows(int r, int nreq) {
+  return r <= 16 ? (nreq > 1 ? 704 : 512) : r <= 32 ? 512 : r <= 64 ? 256 : 192;
+}
 constexpr int LORA_SHORT = 24;
 
 gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
@@ -494,7 +505,7 @@ gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
   // the decode kernel reads rows of X, A and B in 16-byte pieces
   if (!rows16(a.X, a.ldx) || !rows16(a.P, a.K) || !rows16(a.Q, a.r))
     return lora_general(a, bf16, false, s);
-  const bool tc = a.m > lora_decode_rows(a.r) && lora_tc_supported(a, false);
+  const bool tc = a.m > lora_decode_rows(a.r, a.nreq) && lora_tc_supported(a, false);
   if (tc) {
     // the long requests first, the short ones beside them on the SMs that are left
     if (a.nreq > 1) a.min_len = LORA_SHORT + 1;

@@ -1,4 +1,5 @@
-"""Infinities that meet the padding of the adapters' rank."""
+"""Infinities that meet the padding of the adapters' rank, and batches at the sizes where another
+kernel takes over."""
 
 import pytest
 import torch
@@ -50,3 +51,19 @@ def test_infinity_in_a_row(lens, rank, dtype):
     for row, want in ((hit[0], inf), (hit[2], -inf)):
         assert (got[row] == want).all()
     R.check(got[keep], ref[keep], bound[keep], "dX")
+
+
+@pytest.mark.parametrize("rank,rows", [(8, 512), (16, 512), (32, 512), (64, 256), (128, 192)])
+@pytest.mark.parametrize("several", [False, True])
+def test_batches_at_the_rule(rank, rows, several):
+    # on both sides of the number of rows where the tensor-core kernel takes over
+    from post_weight_quantization_23_b200 import lora_add
+    edges = [rows, rows + 1] if rank > 16 or not several else [704, 705]
+    for m in edges:
+        lens, ids = ([m - 100, 99, 1], [1, 0, 1]) if several else ([m], [1])
+        s = R.make(BF, 512, 328, rank, 2, lens, ids, m)
+        ref, bound, Vr, bv, _ = R.add_ref(s, BF)
+        V = torch.zeros(m, rank, device="cuda")
+        out = lora_add(s["Y"], s["X"], *_args(s), out=torch.empty_like(s["Y"]), V=V)
+        R.check(out, ref, bound, "out")
+        R.check(V, Vr, bv, "V")
