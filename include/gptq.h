@@ -397,8 +397,14 @@ GPTQ_API gptq_status gptq_gemm_dgrad(const void* dY, gptq_dtype dt, int64_t m, i
  *   V        (m, rank) fp32 out or NULL: what gptq_lora_backward needs (0 for rows
  *            of a request without an adapter).
  *   m < 2^27, nreq <= m + 65536.  The library allocates nothing; sums run in a fixed order.
+ * Kernel choice: rows of X, A and B on 16-byte boundaries take the decode kernel
+ * (small batches, and short requests of larger ones) or the tensor-core kernel
+ * (Y's rows on 16-byte boundaries too); everything else the general kernel, one
+ * CTA per row on the CUDA cores.
  * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_UNSUPPORTED (rank, f32),
- * GPTQ_ERR_CUDA.  m == 0, n == 0, nreq == 0: no-op. */
+ * GPTQ_ERR_CUDA.  m == 0, n == 0, nreq == 0: no-op.  The call does not wait for
+ * the device: a bounded wait of the tensor-core kernel that gave up shows as NaN
+ * in out and V, over the rows with an adapter that the CTA's cluster had left. */
 GPTQ_API gptq_status gptq_lora_add(const void* Y, int64_t ldy, const void* X, gptq_dtype dt,
                       int64_t m, int64_t k, int64_t ldx, const void* A, const void* B,
                       const float* scaling, int64_t na, int rank, const int32_t* starts,
@@ -425,8 +431,15 @@ GPTQ_API gptq_status gptq_lora_add(const void* Y, int64_t ldy, const void* X, gp
  *            dY, X or V makes the sums that it enters NaN or infinite (an
  *            infinity may give NaN: the factors enter in two parts), no others.
  *   ws       GPTQ_OP_LORA_BACKWARD workspace.
+ * Kernel choice: tensor cores for U and out where rows of dY, A, B and dX lie on
+ * 16-byte boundaries, for dA where rows of X do (codes: ldx a multiple of 16),
+ * for dB where rows of dY and V do; the general kernels on the CUDA cores, each
+ * on its own, elsewhere.
  * Returns GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_UNSUPPORTED (rank, f32),
- * GPTQ_ERR_WORKSPACE, GPTQ_ERR_CUDA. */
+ * GPTQ_ERR_WORKSPACE, GPTQ_ERR_CUDA.  A bounded wait of a tensor-core kernel that
+ * gave up shows as NaN: in out over the rows with an adapter that the CTA's
+ * cluster had left (and in the dA that such rows enter), in dA or dB over the
+ * CTA's columns. */
 GPTQ_API gptq_status gptq_lora_backward(const void* dY, gptq_dtype dt, int64_t m, int64_t n,
                       int64_t lddy, const void* X, int64_t ldx, const float* x_scales, int64_t k,
                       const float* V, const void* A, const void* B, const float* scaling,

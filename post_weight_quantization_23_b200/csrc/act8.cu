@@ -14,8 +14,9 @@
 // 8-byte store), 16 neighbouring lanes a block, so every access of a warp is
 // contiguous and the maximum takes four shuffles; four vectors per thread are
 // requested before the first is used.  8192 x 11008 bf16
-// saved and restored: 94 us (547 MB, 5.8 TB/s, 0.90 of measured HBM); with scalar maxima
-// and both divisions in every lane the save alone took 91 us, its instructions the bound.
+// saved and restored: 94 us in a replayed graph (547 MB, 5.8 TB/s, 0.90 of measured HBM; 101 us
+// through the two Python calls); with scalar maxima and both divisions in every lane the save
+// alone took 91 us, its instructions the bound.
 #include "common.cuh"
 
 #include <algorithm>
@@ -32,7 +33,8 @@ constexpr int A8_UNROLL = 4;       // vectors in flight per thread
 // must stay finite)
 constexpr float A8_TINY = 7.8886090522101181e-31f;  // 2^-100
 
-// Division by a fixed number below 2^31 as a multiplication: n / d for n < 2^31.
+// Division by a fixed number below 2^31 as a multiplication, n / d for n < 2^31 (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994).
 struct A8Div {
   uint32_t mul, shift;
 };

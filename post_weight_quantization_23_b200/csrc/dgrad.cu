@@ -37,8 +37,9 @@
 // distributed shared memory in a fixed order; launch_shape picks MT, N and the split.
 // Every wait is bounded; a CTA that gives up drains its copies and MMAs, frees TMEM and
 // writes NaN over its outputs.
-// 22016 x 4096, 4096 tokens: 600 us, 1230 TFLOP/s, 0.72 of the measured bf16 burst (690 us
-// in a long run, under the power cap); 4096 x 4096, 512 tokens: 29 us.
+// 22016 x 4096, 4096 tokens, bf16: 605 us, 1220 TFLOP/s, 0.71 of the measured bf16 burst (690 us
+// in a long run, under the power cap), f16 625; 4096 x 4096, 512 tokens: 30 us (f16 30.5, and
+// 64 with scales of 1e-6, which take the second pass).
 #include "cluster.cuh"
 #include "tc_ptx.cuh"
 

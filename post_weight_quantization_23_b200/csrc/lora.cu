@@ -191,10 +191,11 @@ __device__ __forceinline__ int ld_piece(const LdWindow& w, int p, LdShared& sm) 
 //      first scaled by a power of two, so that neither leaves the type's range).
 // Latency is what it spends its time on, so the tiles of B and Y are requested several at a
 // time, the first of them before the barrier.  One launch, no workspace, sums in a fixed order.
-// One token, rank 16, 4096 -> 4096: 4.9 us (look-up 1.2, loads of A 1.0, sums and exchange
-// 1.2, output 0.6; the rest launch); 64 tokens over 16 adapters, 4096 -> 12288: 10.0 us
-// (a piece per token, each adapter read four times: 14.4; three CTAs an SM, with fewer tiles
-// of B in flight and more clusters that find no piece: 11.7).
+// In a replayed graph: one token, rank 16, 4096 -> 4096 4.4 us (look-up 1.2, loads of A 1.0, sums
+// and exchange 1.2, output 0.6; the rest launch); 64 tokens over 16 adapters, 4096 -> 12288 9.4 us
+// (before the latest steps, when it took 10.0: a piece per token, each adapter read four times,
+// 14.4; three CTAs an SM, with fewer tiles of B in flight and more clusters that find no piece,
+// 11.7).
 template <bool BF16, int RP>
 __global__ void __launch_bounds__(LD_THREADS, RP <= 64 ? 2 : 1)
 lora_decode_kernel(LoraArgs a, int yvec, int late) {
@@ -507,7 +508,8 @@ gptq_status lora_add_impl(LoraArgs a, bool bf16, cudaStream_t s) {
     return lora_general(a, bf16, false, s);
   const bool tc = a.m > lora_decode_rows(a.r, a.nreq) && lora_tc_supported(a, false);
   if (tc) {
-    // the long requests first, the short ones beside them on the SMs that are left
+    // the long requests first, the short ones beside them on the SMs that are left (the lengths
+    // are on the device: with several requests both kernels are launched, whatever they find)
     if (a.nreq > 1) a.min_len = LORA_SHORT + 1;
     const gptq_status st = lora_tc(a, bf16, false, s);
     if (st != GPTQ_OK || a.nreq == 1) return st;

@@ -13,9 +13,10 @@
 //   W is split into two bf16 parts, hi + lo (16 significant bits; bf16 for its range:
 //     gradients are small, f16 would lose them among its subnormals), side by side as one
 //     operand of 2 RP columns: S is read from shared memory, whose bandwidth sets the
-//     pace, once for both, and the two halves of D are added at the end.
+//     pace, once for both, and the two halves of D are added at the end.  What the split
+//     leaves, 2^-17 of W, is far below the result's rounding (2^-9, f16 2^-12).
 //   S in bf16 is used as it is.  S in f16 is split into two bf16 parts as well (exactly),
-//     three products, lo x lo left out.
+//     three products: lo x lo, 2^-17 of a product at most, is not worth a fourth MMA.
 //   S in 8-bit codes becomes bf16 exactly (|code| <= 127), and its scales, one per token
 //     and 128-column block, multiply the rows of W: the checkpoint is never restored.
 // Tiles to be converted land in a ring of their own, deeper than the operands' (a tile of
@@ -27,9 +28,11 @@
 // slot belongs to one group, which sees every phase of its barrier (a wait that skips
 // phases cannot tell the one before from the one it wants).
 // Every wait is bounded; a CTA that gives up writes NaN.
-// 4096 tokens, rank 64, 4096 x 11008 from codes: 51 us.  A CTA of the code columns takes 1000
-// cycles per 64-token tile (conversion of codes and W, some 2000 warp instructions), one of
-// the bf16 columns 700 to 900 (copies' latency); at HBM's rate the kernel's 108 MB take 17 us.
+// 4096 tokens, rank 64, 4096 x 11008 from codes: 52 us alone, 46 with X in bf16; 8192 tokens
+// 92 and 82.  So a 64-token tile takes 1100 cycles where there are columns of codes (conversion
+// of codes and W, some 2000 warp instructions) and 980 in bf16 (copies' latency), and what does
+// not grow with the tokens is 12 us (64 tokens alone: 14; launch, look-up, TMEM, first copies,
+// sums, stores).  At HBM's rate the 108 MB of 4096 tokens take 17 us.
 #include "lora.cuh"
 #include "tc_ptx.cuh"
 

@@ -15,8 +15,9 @@
 //   2. Exchange through distributed shared memory: each CTA hands its partial sums
 //      to the CTA that owns the row (128 / CS rows each, in eights); the owner adds them in a
 //      fixed order, scales, and hands V to all.  V as hi + lo of the 16-bit type
-//      (f16: each row scaled by a power of two, taken back exactly) becomes the A
-//      operand of
+//      (f16: each row scaled by a power of two, taken back exactly; the MMA takes A and B of
+//      one type, and two parts leave u^2 of V, far below the u of the rounded result, where
+//      one would add u) becomes the A operand of
 //   3. CTA q takes every CS-th 64-column tile of the output, D2[128 x 64] in a TMEM
 //      buffer per epilogue group; the tile of Y arrives by TMA beside Q, the sum is rounded once
 //      and stored row by row (a TMA store would also write rows of the next request).
@@ -27,7 +28,8 @@
 // leaves no shared memory for the second operand and takes the steps in turn).
 // Warps: 0 TMA, 1 MMA, 2..5 exchange, 6..17 epilogue (three groups of four, tile by tile
 // in turn, a TMEM buffer each).
-// 8192 tokens, rank 64, 4096 -> 11008: 89 us (432 MB, 4.8 TB/s, 0.75 of measured HBM): its
+// 8192 tokens, rank 64, 4096 -> 11008: 89 us in a replayed graph, the caller's zero-fill of V
+// included (432 MB, 4.8 TB/s, 0.75 of measured HBM; 96 us through the Python call): its
 // two rounds of output tiles run at 5.8 TB/s, the first reduction and exchange (22 us) before
 // them are half covered by the second reduction.  Two epilogue groups instead of three: 83
 // -> 87 us for 3001 ragged f16 tokens at rank 8; asking for tiles in L2 ahead changed nothing.
