@@ -24,7 +24,7 @@ U = {H: 2.0 ** -11, BF: 2.0 ** -8}
 # (n, k, group, m) and the tile shape they are here for
 ONE = (304, 1056, 128, 17)        # one 128-column tile per CTA
 SPLIT = (4104, 384, 64, 200)      # the rows of W shared by the CTAs of a cluster
-TWO = (712, 7200, 96, 1000)       # two 128-column tiles per CTA, ragged everywhere
+TWO = (1000, 7200, 96, 1000)      # two 128-column tiles per CTA, ragged everywhere
 GENERAL = (301, 320, 32, 33)      # odd n: rows of dY off 16 bytes
 
 
