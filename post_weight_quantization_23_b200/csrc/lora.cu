@@ -193,9 +193,8 @@ __device__ __forceinline__ int ld_piece(const LdWindow& w, int p, LdShared& sm) 
 // time, the first of them before the barrier.  One launch, no workspace, sums in a fixed order.
 // In a replayed graph: one token, rank 16, 4096 -> 4096 4.4 us (look-up 1.2, loads of A 1.0, sums
 // and exchange 1.2, output 0.6; the rest launch); 64 tokens over 16 adapters, 4096 -> 12288 9.4 us
-// (before the latest steps, when it took 10.0: a piece per token, each adapter read four times,
-// 14.4; three CTAs an SM, with fewer tiles of B in flight and more clusters that find no piece,
-// 11.7).
+// (half as long again with a piece per token, each adapter read four times; a sixth more with
+// three CTAs an SM, fewer tiles of B in flight and more clusters that find no piece).
 template <bool BF16, int RP>
 __global__ void __launch_bounds__(LD_THREADS, RP <= 64 ? 2 : 1)
 lora_decode_kernel(LoraArgs a, int yvec, int late) {
